@@ -1,6 +1,8 @@
 /*
  * mnb.h -- C ABI of the GB300 (sm_103a) library for block-quantized
- * weight-only matmul (MatMulNBits) and the QMoE expert FFN built on it.
+ * weight-only matmul (MatMulNBits), the QMoE expert FFN built on it, and what
+ * a decoder needs around them to generate: a paged key-value cache, attention
+ * over it, and the verification of drafted tokens.
  *
  * Shared conventions
  * ------------------
@@ -339,6 +341,138 @@ mnb_status qmoe_route(const float* logits, int64_t T, int64_t E, int k, int norm
  * the caller; E <= 1024, T*k < 2^31. */
 mnb_status qmoe_permute(const int32_t* topk_idx, int64_t T, int k, int64_t E, int32_t* counts,
                         int32_t* offsets, int32_t* perm, mnb_stream_t stream);
+
+/* ------------------------------------- paged key-value cache, attention */
+
+/* Keys and values of many sequences in pages of page_size tokens.  Element
+ * (page, head, row in page, d) of k or v is at page * page_stride + head *
+ * head_stride + row * token_stride + d (strides in elements, the same for k
+ * and v), so that [pages, heads, rows, dim], [pages, rows, heads, dim] and a
+ * k and a v interleaved in one buffer are all described.  dtype f16 or bf16;
+ * head_dim a multiple of 8 in 16..256; page_size a multiple of 8; k, v and
+ * the strides in whole 16-byte units.  The pages quoted above have no cache:
+ * these entry points exist for decoders built on the products. */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t num_pages, page_stride, head_stride, token_stride;
+    int32_t page_size, kv_heads, head_dim;
+    int32_t dtype; /* mnb_dtype */
+} kv_cache_desc;
+
+/* The tokens of one step of a batch of sequences (device arrays; kept by the
+ * caller over all layers of the step).
+ *   seq_lens    [batch]: tokens in the cache once the step's are in it.
+ *   new_start   [batch + 1], not decreasing: sequence b's new tokens are rows
+ *               new_start[b] .. new_start[b+1] - 1 of the step's `tokens`
+ *               rows (prompts, drafted tokens, one token, none).  NULL: one
+ *               token for each sequence (tokens == batch).
+ *   page_table  [batch, max_pages], rows table_stride apart: the page of
+ *               sequence b's tokens i * page_size .. (i + 1) * page_size - 1.
+ *               Entries past a sequence's length are never read into a result.
+ *   max_new     the most new tokens of one sequence, a hint: it sizes the row
+ *               tiles and the workspace of kv_attention; the results are
+ *               right for any number.
+ * New token i of sequence b (n_b of them) has the position seq_lens[b] - n_b +
+ * i; one below zero marks a padding row (a sequence of length 0 in a step of
+ * fixed shape), for which nothing is stored and attention gives zeros.  Rows
+ * outside every sequence are left alone. */
+typedef struct {
+    const int32_t* seq_lens;
+    const int32_t* new_start;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int32_t batch, tokens, max_new, max_pages;
+} kv_step_desc;
+
+/* What happens to queries and keys before they are used.
+ *   q_norm, k_norm  [head_dim] fp32 or NULL: per-head norm x / sqrt(mean(x^2)
+ *                   + eps) * weight, first.
+ *   cos_sin         [max_pos, rot_dim] fp32 or NULL (no rotation): row p holds
+ *                   rot_dim / 2 cosines, then as many sines, of position p's
+ *                   angles; the pair (a, b) of angle i becomes (a cos - b sin,
+ *                   b cos + a sin).  Pairs are (i, i + rot_dim / 2), or (2i, 2i
+ *                   + 1) when interleaved != 0; elements past rot_dim keep
+ *                   their values.  rot_dim a multiple of 8, at most head_dim.
+ * All 16-byte aligned. */
+typedef struct {
+    const float* cos_sin;
+    int64_t max_pos;
+    int32_t rot_dim, interleaved;
+    const float* q_norm;
+    const float* k_norm;
+    float eps;
+} kv_rope_desc;
+
+/* Stores a step's keys and values in the cache and writes its queries to
+ * q_out, keys and queries normed and rotated as *rope says (NULL: neither).
+ * q [tokens, q_heads, head_dim], k and v [tokens, kv_heads, head_dim] in dtype
+ * (f32 or the cache's), each with its own stride in elements between tokens,
+ * so that they may be parts of one projection's output rows; q_out like q, and
+ * may be q itself.  q and q_out may both be NULL.  Computed in fp32, rounded
+ * once to the cache's dtype (q_out: to dtype).  A token whose position has no
+ * page (a page number outside [0, num_pages), a position past max_pages *
+ * page_size) or no row of cos_sin is skipped, with its q_out row, and records
+ * MNB_ERR_CONTENT in the device error word.  Pointers and strides in whole
+ * 16-byte units (strides: multiples of 8 elements). */
+mnb_status kv_append(const kv_cache_desc* cache, const kv_step_desc* step, const kv_rope_desc* rope, const void* q,
+                     int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, mnb_dtype dtype, void* q_out, int64_t q_out_stride, mnb_stream_t stream);
+
+/* Bytes of device workspace kv_attention needs: the partial results of
+ * sequences that are split over the GPU.  Depends only on the arguments. */
+mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_new,
+                                       size_t* bytes);
+
+/* Attention of a step's new tokens over the cache (which holds them already:
+ * kv_append first).  Row (token at position p of sequence b, query head h)
+ * sees the cached tokens j <= p of its sequence, with window > 0 only those
+ * with j > p - window:
+ *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale q . k_j,
+ * m the largest s_j; query head h reads key-value head h / (q_heads /
+ * kv_heads).  A row that sees nothing gives zeros.  lse [tokens, q_heads] (or
+ * NULL) gets m + ln(sum), -infinity for such a row.
+ * q, out [tokens, q_heads, head_dim] in dtype (f32 or the cache's) with strides
+ * in elements between tokens, whole 16-byte units.  scale > 0 and finite.
+ * Scores, statistics and sums are fp32; the probabilities carry at least 16
+ * significant bits (fp32 output: 22) into the product with the values.  The
+ * results do not depend on which other sequences share the step in more than
+ * the order of fp32 additions, and are the same on every run.  What the cache
+ * holds in places a row does not see never reaches it, NaN and infinities
+ * included.  A page number outside [0, num_pages) within a sequence's length
+ * reads as zeros and records MNB_ERR_CONTENT; a length past max_pages *
+ * page_size is cut there.
+ * Made for a few new tokens per sequence (decoding, drafts): one pass over the
+ * cache serves 64 rows, so that a prompt is right but re-reads it.  workspace
+ * 256-byte aligned. */
+mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, const void* q, int64_t q_stride,
+                        int64_t q_heads, mnb_dtype dtype, void* out, int64_t out_stride, float* lse, float scale,
+                        int64_t window, void* workspace, size_t workspace_bytes, mnb_stream_t stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given uniform numbers in [0, 1).  Sequence b has n = n_drafts[b] drafts (NULL:
+ * all `drafts` of them; cut to 0..drafts).  Draft i, token x, stands while
+ * uniforms[b, i] * q < p with p = target[b, i, x], q = draft[b, i, x] (fp32
+ * product).  After the first draft r that falls the next token is drawn from
+ * max(target[b, r] - draft[b, r], 0), after the last from target[b, n], by
+ * uniforms[b, drafts]: with w_i = floor(2^40 min(weight_i, 1)) (a NaN counts
+ * as 0) and U = floor(2^24 uniform), the smallest i with w_0 + .. + w_i >
+ * floor(U sum(w) / 2^24).  The sums are whole numbers: the draw is exact and
+ * does not depend on how the vocabulary is split.  draft == NULL: drafts
+ * without probabilities (q = 1; the fallen token is left out of target[b, r]).
+ * Where nothing is left of the weights, target[b, r] itself is drawn from.
+ *   target [batch, drafts + 1, vocab], draft [batch, drafts, vocab] fp32 with
+ *   strides in elements between sequences and rows (0 shares a row); draft_tokens [batch,
+ *   drafts]; uniforms [batch, drafts + 1]; drafts may be 0 (plain sampling).
+ *   tokens [batch, drafts + 1] out: the standing drafts, the drawn token, -1s;
+ *   accepted [batch] out: how many drafts stand.
+ * A draft token outside [0, vocab) falls and records MNB_ERR_CONTENT; a row
+ * without any probability gives the token -1 and records it too.  vocab <
+ * 2^22, drafts <= 1024, else MNB_ERR_UNSUPPORTED. */
+mnb_status draft_verify(const float* target, int64_t target_seq_stride, int64_t target_row_stride, const float* draft,
+                        int64_t draft_seq_stride, int64_t draft_row_stride, const int32_t* draft_tokens,
+                        const int32_t* n_drafts, const float* uniforms, int64_t batch, int64_t drafts, int64_t vocab,
+                        int32_t* tokens, int32_t* accepted, mnb_stream_t stream);
 
 /* ------------------------------------------------------ diagnostics, tools */
 

@@ -33,6 +33,28 @@ class PrepackedDesc(ctypes.Structure):
                 ("identity", ctypes.c_uint64)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    """kv_cache_desc: a paged key-value cache (see kv_cache)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KvStepDesc(ctypes.Structure):
+    """kv_step_desc: the new tokens of one step (see kv_step)."""
+    _fields_ = [("seq_lens", ctypes.c_void_p), ("new_start", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class KvRopeDesc(ctypes.Structure):
+    """kv_rope_desc: per-head norms and position rotation (see kv_rope)."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 class MnbError(RuntimeError):
     def __init__(self, status: int, call: str):
         super().__init__(f"{call} failed: {STATUS.get(status, status)}")
@@ -62,6 +84,10 @@ _SIGNATURES = {
                             _P, _P],
     "qmoe_route": [_P, _I64, _I64, _I, _I, _P, _P, _P],
     "qmoe_permute": [_P, _I64, _I, _I64, _P, _P, _P, _P],
+    "kv_append": [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P],
+    "kv_attention_workspace_size": [_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)],
+    "kv_attention": [_P, _P, _P, _I64, _I64, _I, _P, _I64, _P, ctypes.c_float, _I64, _P, _SZ, _P],
+    "draft_verify": [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P],
     "mnb_unpack_codes": [_P, _I64, _I64, _I, _I, _P, _P],
     "mnb_pack_codes": [_P, _I64, _I64, _I, _I, _P, _P],
     "mnb_quantize_int3": [_P, _I, _I64, _I64, _I, _P, _P, _I, _P],
@@ -352,6 +378,175 @@ def qmoe_permute(topk_idx, E, counts, offsets, perm, stream=None, *, T=None, k=N
                                      _stream(stream))
     if check:
         _check(st, "qmoe_permute")
+    return st
+
+
+def _on_gpu(t, name, dtype=None):
+    """The data pointer of a CUDA tensor (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _packed(t, name, dtype):
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _on_gpu(t, name, dtype)
+
+
+def kv_cache(k, v) -> KvCacheDesc:
+    """Describes a paged cache held in k and v [pages, kv_heads, page_size, head_dim] (f16 or bf16; any strides
+    with unit stride along head_dim, the same for both: permuted views describe other layouts)."""
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
+        raise ValueError("k and v must be 4-D tensors of one shape, dtype and layout")
+    if k.stride(3) != 1:
+        raise ValueError("the head dimension must have unit stride")
+    d = KvCacheDesc(_on_gpu(k, "k"), _on_gpu(v, "v"), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[2],
+                    k.shape[1], k.shape[3], _dtype_code(k))
+    d.tensors = (k, v)  # kept alive with the descriptor
+    return d
+
+
+def kv_step(seq_lens, page_table, new_start=None, tokens=None, max_new=1) -> KvStepDesc:
+    """Describes a step's new tokens: seq_lens int32 [batch] (with the new tokens), page_table int32 [batch,
+    max_pages] (unit stride along pages), new_start int32 [batch + 1] or None for one token per sequence (then
+    `tokens` is the batch).  max_new: the most new tokens of one sequence."""
+    import torch
+    batch = seq_lens.shape[0]
+    if tokens is None:
+        if new_start is not None:
+            raise ValueError("tokens must be given with new_start")
+        tokens = batch
+    if page_table.dim() != 2 or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [batch, max_pages] with unit stride along the pages")
+    if new_start is not None and new_start.numel() != batch + 1:
+        raise ValueError("new_start must have batch + 1 elements")
+    stride = page_table.stride(0) if batch > 1 else max(page_table.shape[1], 1)
+    d = KvStepDesc(_packed(seq_lens, "seq_lens", torch.int32), _packed(new_start, "new_start", torch.int32),
+                   _on_gpu(page_table, "page_table", torch.int32), stride, batch, tokens, max_new,
+                   page_table.shape[1])
+    d.tensors = (seq_lens, new_start, page_table)
+    return d
+
+
+def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e-6) -> KvRopeDesc:
+    """Describes the rotation (cos_sin f32 [max_pos, rot_dim]: cosines, then sines) and the per-head norms (f32
+    [head_dim]) of queries and keys; None leaves a part out."""
+    import torch
+    max_pos, rot_dim = (0, 0) if cos_sin is None else cos_sin.shape
+    d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32), max_pos, rot_dim, int(bool(interleaved)),
+                   _packed(q_norm, "q_norm", torch.float32), _packed(k_norm, "k_norm", torch.float32), eps)
+    d.tensors = (cos_sin, q_norm, k_norm)
+    return d
+
+
+def _token_rows(t, name, tokens, heads, dim):
+    """Pointer and token stride of [tokens, heads, head_dim] rows (heads adjacent within a token)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name} must be [{tokens}, {heads or 'heads'}, {dim}], not {list(shape)}")
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
+        raise ValueError(f"the heads of a token of {name} must be adjacent")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr(), (stride[0] if tokens > 1 else max(shape[1] * dim, 8))
+
+
+def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True):
+    """Stores a step's k and v [tokens, kv_heads, head_dim] in the cache and writes q [tokens, q_heads, head_dim] to
+    q_out (may be q; both None: no queries), q and k normed and rotated as `rope` says.  Rows may be strided parts
+    of one projection's output."""
+    n, dim = step.tokens, cache.head_dim
+    kp, ks = _token_rows(k, "k", n, cache.kv_heads, dim)
+    vp, vs = _token_rows(v, "v", n, cache.kv_heads, dim)
+    qp = op = None
+    qs = os_ = heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        qp, qs = _token_rows(q, "q", n, None, dim)
+        if q_out is not None:
+            op, os_ = _token_rows(q_out, "q_out", n, heads, dim)
+            if q_out.dtype != q.dtype:
+                raise TypeError("q_out must have q's dtype")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have one dtype")
+    st = load_library().kv_append(ctypes.byref(cache), ctypes.byref(step), None if rope is None else ctypes.byref(rope),
+                                  qp, qs, heads, kp, ks, vp, vs, _dtype_code(k), op, os_, _stream(stream))
+    if check:
+        _check(st, "kv_append")
+    return st
+
+
+def kv_attention_workspace_size(q_heads, kv_heads, head_dim, max_new=1) -> int:
+    out = _SZ(0)
+    _check(load_library().kv_attention_workspace_size(q_heads, kv_heads, head_dim, max_new, ctypes.byref(out)),
+           "kv_attention_workspace_size")
+    return out.value
+
+
+def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, lse=None, stream=None, check=True):
+    """Attention of the step's new tokens q [tokens, q_heads, head_dim] over the cache into out (same shape and
+    dtype); scale defaults to head_dim ** -0.5, lse (f32 [tokens, q_heads]) is optional."""
+    n, dim, heads = step.tokens, cache.head_dim, q.shape[1]
+    qp, qs = _token_rows(q, "q", n, None, dim)
+    op, os_ = _token_rows(out, "out", n, heads, dim)
+    if out.dtype != q.dtype:
+        raise TypeError("out must have q's dtype")
+    lp = None
+    if lse is not None:
+        import torch
+        lp = _packed(lse, "lse", torch.float32)
+        if lse.numel() != n * heads:
+            raise ValueError("lse must be [tokens, q_heads]")
+    if workspace is None:
+        import torch
+        workspace = torch.empty(kv_attention_workspace_size(heads, cache.kv_heads, dim, step.max_new),
+                                dtype=torch.uint8, device=q.device)
+    st = load_library().kv_attention(ctypes.byref(cache), ctypes.byref(step), qp, qs, heads, _dtype_code(q), op, os_,
+                                     lp, dim ** -0.5 if scale is None else scale, window,
+                                     _packed(workspace, "workspace", None), workspace.nbytes, _stream(stream))
+    if check:
+        _check(st, "kv_attention")
+    return st
+
+
+def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_drafts=None, stream=None, check=True):
+    """Verifies draft_tokens int32 [batch, n] against target f32 [batch, n + 1, vocab] (draft f32 [batch, n, vocab], or
+    None for drafts without probabilities) with uniforms f32 [batch, n + 1]; writes tokens int32 [batch, n + 1]
+    (standing drafts, the drawn token, -1s) and accepted int32 [batch]."""
+    import torch
+    batch, rows, vocab = target.shape
+    f32, i32 = torch.float32, torch.int32
+    if draft is not None and draft.shape != (batch, rows - 1, vocab):
+        raise ValueError("draft must be [batch, n, vocab]")
+    if rows == 1:
+        draft = None  # nothing was drafted
+    for t, name in ((target, "target"), (draft, "draft")):
+        if t is not None and vocab > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name} must have unit stride along the vocabulary")
+    for t, shape, name in ((draft_tokens, (batch, rows - 1), "draft_tokens"), (uniforms, (batch, rows), "uniforms"),
+                           (tokens, (batch, rows), "tokens"), (accepted, (batch,), "accepted"),
+                           (n_drafts, (batch,), "n_drafts")):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+
+    def strides(t, n):  # those of an extent of one are never used
+        return (t.stride(0) if batch > 1 else n * vocab), (t.stride(1) if n > 1 else vocab)
+    ts, tr = strides(target, rows)
+    ds, dr = (0, 0) if draft is None else strides(draft, rows - 1)
+    st = load_library().draft_verify(_on_gpu(target, "target", f32), ts, tr, _on_gpu(draft, "draft", f32), ds, dr,
+                                     _packed(draft_tokens, "draft_tokens", i32), _packed(n_drafts, "n_drafts", i32),
+                                     _packed(uniforms, "uniforms", f32), batch, rows - 1, vocab,
+                                     _packed(tokens, "tokens", i32), _packed(accepted, "accepted", i32),
+                                     _stream(stream))
+    if check:
+        _check(st, "draft_verify")
     return st
 
 

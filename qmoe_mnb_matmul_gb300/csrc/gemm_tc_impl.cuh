@@ -49,17 +49,14 @@
 // wavefront per lane.  Every wait is bounded.
 #pragma once
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
 #include "gemv_core.cuh"
 #include "kernels.h"
+#include "tensor_map.h"
 
 namespace mnb {
 
@@ -732,20 +729,6 @@ __global__ void __launch_bounds__(kThreadsTC, 1) gemm_tc_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------- host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // Ring depths: kWeightSlots dequantised-weight slots, and as many activation
 // slots as fit (up to kMaxStagesTC).  A group waits on the weight slot of its

@@ -1,0 +1,118 @@
+// kv.h -- arguments and host-side launchers of the paged key-value cache
+// kernels and of the draft verification (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mnb.h"
+
+namespace mnb {
+
+// The paged cache: element (page, head, row in page, d) of keys or values is at
+// page * page_stride + head * head_stride + row * token_stride + d.
+struct KvCache {
+    void* k;
+    void* v;
+    int64_t num_pages, page_stride, head_stride, token_stride;  // strides in elements
+    int page_size, heads, dim, dtype;
+};
+
+// One step's tokens (device arrays of the caller).
+struct KvStep {
+    const int* seq_lens;    // [batch] tokens in the cache after the step
+    const int* new_start;   // [batch + 1], or null: token b belongs to sequence b
+    const int* page_table;  // [batch, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int batch, tokens, max_pages;
+    int capacity;           // min(max_pages * page_size, 2^31 - 1)
+};
+
+// First new token and number of new tokens of sequence b, kept inside
+// [0, tokens] whatever new_start holds.
+__device__ __forceinline__ void step_tokens(const KvStep& s, int b, int* first, int* count) {
+    if (s.new_start == nullptr) {
+        *first = b;
+        *count = 1;
+        return;
+    }
+    const int lo = min(max(__ldg(s.new_start + b), 0), s.tokens);
+    const int hi = min(max(__ldg(s.new_start + b + 1), 0), s.tokens);
+    *first = lo;
+    *count = max(hi - lo, 0);
+}
+
+// ------------------------------------------------------------- kv_append
+
+struct KvAppendArgs {
+    KvCache cache;
+    KvStep step;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int q_heads, in_dtype;
+    void* q_out;
+    int64_t q_out_stride;
+    const float* cos_sin;  // [max_pos, rot_dim]: rot_dim / 2 cosines, then as many sines; null: no rotation
+    int64_t max_pos;
+    int rot_dim, interleaved;
+    const float *q_norm, *k_norm;  // [dim] or null
+    float eps;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream);
+cudaError_t kv_append_take_error(unsigned int* out);
+
+// ---------------------------------------------------------- kv_attention
+
+constexpr int kKvTile = 64;      // cached tokens per tile
+constexpr int kKvMaxCtas = 304;  // CTAs of the main kernel: two on each of 152 SMs
+
+struct KvAttnArgs {
+    KvCache cache;
+    KvStep step;
+    const void* q;
+    int64_t q_stride;
+    void* out;
+    int64_t out_stride;
+    float* lse;  // [tokens, q_heads] or null
+    int group;   // query heads per key-value head
+    float scale;
+    int window;  // 0: every earlier token
+    int box_rows;
+    // partial results of the pairs split over CTAs: two slots per CTA
+    float* part_o;     // [2 * ctas][rows][padded dim]
+    float2* part_ml;   // [2 * ctas][rows]: running maximum (log2 units), sum
+    // [ctas][2]: the pair that begins in this CTA and goes on in later ones:
+    // {last CTA (-1: no such pair), slot of its part here, first row (token * group + head in group), rows}, {head, -, -, -}
+    int4* join;
+};
+
+// Rows of a row tile (16, 32 or 64) and the head dimension's padded width.
+int kv_attention_rows(int group, int64_t max_new);
+int kv_attention_pad(int dim);
+struct KvAttnSpace {
+    int64_t part_o, part_ml, join, total;  // byte offsets, bytes
+};
+KvAttnSpace kv_attention_space(int rows, int pad);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, int q_dtype, int64_t max_new, void* workspace, int sm_count,
+                                bool pdl, cudaStream_t stream);
+cudaError_t kv_attention_take_error(unsigned int* out);
+
+// ---------------------------------------------------------- draft_verify
+
+struct DraftArgs {
+    const float* target;  // [batch][drafts + 1][vocab], sequence and row strides in elements
+    int64_t target_seq, target_row;
+    const float* draft;   // [batch][drafts][vocab] or null
+    int64_t draft_seq, draft_row;
+    const int* draft_tokens;  // [batch, drafts]
+    const int* n_drafts;      // [batch] or null
+    const float* uniforms;    // [batch, drafts + 1]
+    int64_t batch, vocab;
+    int drafts;
+    int* tokens;              // [batch, drafts + 1]
+    int* accepted;            // [batch]
+};
+cudaError_t launch_draft_verify(const DraftArgs& a, int sm_count, bool pdl, cudaStream_t stream);
+cudaError_t draft_take_error(unsigned int* out);
+
+}  // namespace mnb

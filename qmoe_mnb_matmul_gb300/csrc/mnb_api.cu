@@ -2,13 +2,13 @@
 // host-side metadata validation (payloads are never read on the host), plan
 // selection and kernel launches on the caller's stream.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
+#include "api_util.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv.h"
 #include "qmoe.h"
 
 namespace mnb {
@@ -18,50 +18,11 @@ namespace {
 // Smallest M routed to the tensor-core GEMM (fp16/bf16 activations only).
 constexpr int64_t kTcMinRows = 16;
 
-bool valid_dtype(int d) { return d == MNB_F32 || d == MNB_F16 || d == MNB_BF16; }
 bool valid_bits(int b) { return b == 3 || b == 4; }
 // mnb_matmul / mnb_matmul_int8a: every width of the row-local LSB-first format
 // (3 and 4 on every path; 1, 2 and 5..8 on the CUDA-core path for any M)
 bool valid_bits_any(int b) { return b >= 1 && b <= 8; }
 bool valid_bs(int bs) { return bs == 32 || bs == 64 || bs == 128; }
-size_t dsize(int d) { return d == MNB_F32 ? 4 : 2; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// a * b without overflow past 2^62 (the largest byte count we accept).
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > (int64_t(1) << 62) / a) return false;
-    *out = a * b;
-    return true;
-}
-
-int sm_count_current() {
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) {
-        const int c = cache[dev].load(std::memory_order_relaxed);
-        if (c > 0) return c;
-    }
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
-// Programmatic dependent launch is on unless MNB_DISABLE_PDL is set in the
-// environment (for tools that replay kernels one by one).
-bool pdl_enabled() {
-    static const bool on = std::getenv("MNB_DISABLE_PDL") == nullptr;
-    return on;
-}
-
-mnb_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return MNB_OK;
-    if (e == cudaErrorNotSupported) return MNB_ERR_UNSUPPORTED;
-    return MNB_ERR_CUDA;
-}
-
 // Byte counts of one packed projection [N, K]; false on overflow.
 struct ProjBytes {
     int64_t nb, row_bytes, weight, scales, zp_row, zp;
@@ -120,7 +81,8 @@ mnb_status mnb_get_last_device_error(mnb_stream_t stream) {
     unsigned int first = 0;
     cudaError_t (*takers[])(unsigned int*) = {gemv_take_error, gemv_pp_take_error, qmoe_take_error,
                                               gemm_tc_take_error, quant_take_error, diag_take_error,
-                                              qmoe_decode_take_error};
+                                              qmoe_decode_take_error, kv_append_take_error,
+                                              kv_attention_take_error, draft_take_error};
     for (auto take : takers) {
         unsigned int v = 0;
         if (take(&v) != cudaSuccess) return MNB_ERR_CUDA;
