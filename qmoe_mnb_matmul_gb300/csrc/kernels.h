@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace mnb {
@@ -26,6 +27,31 @@ inline cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, size
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// launch_ex of a kernel whose dynamic shared memory and carveout are set at its
+// first launch on a device and not at every call (the two attribute calls cost
+// about as much host time as a launch).  A device that was reset has lost them:
+// a launch that fails sets them again and is tried once more.
+template <auto Kern, typename... Args>
+inline cudaError_t launch_ready(dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl, const Args&... args) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) {
+        if ((e = launch_ex(Kern, grid, block, smem, stream, pdl, args...)) == cudaSuccess) return e;
+        cudaGetLastError();
+    }
+    if (smem > 0)
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 static_cast<int>(cudaSharedmemCarveoutMaxShared));
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return launch_ex(Kern, grid, block, smem, stream, pdl, args...);
 }
 
 // ------------------------------------------------------------- SIMT GEMV

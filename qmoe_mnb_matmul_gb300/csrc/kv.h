@@ -66,6 +66,22 @@ cudaError_t kv_append_take_error(unsigned int* out);
 constexpr int kKvTile = 64;      // cached tokens per tile
 constexpr int kKvMaxCtas = 304;  // CTAs of the main kernel: two on each of 152 SMs
 
+// Division by a number fixed at launch: x / d = (hi32(x m) + x) >> s for 0 <= x < 2^31
+// (Granlund and Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+    uint32_t m, s;
+    void set(uint32_t d) {
+        s = 0;
+        while ((uint64_t(1) << s) < d) ++s;
+        m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int x) const {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(x), m) + static_cast<uint32_t>(x)) >> s);
+    }
+#endif
+};
+
 struct KvAttnArgs {
     KvCache cache;
     KvStep step;
@@ -75,18 +91,19 @@ struct KvAttnArgs {
     int64_t out_stride;
     float* lse;  // [tokens, q_heads] or null
     int group;   // query heads per key-value head
+    FastDiv by_group;
     float scale;
     int window;  // 0: every earlier token
     int box_rows;
     // partial results of the pairs split over CTAs: two slots per CTA
     float* part_o;     // [2 * ctas][rows][padded dim]
     float2* part_ml;   // [2 * ctas][rows]: running maximum (log2 units), sum
-    // [ctas][2]: the pair that begins in this CTA and goes on in later ones:
-    // {last CTA (-1: no such pair), slot of its part here, first row (token * group + head in group), rows}, {head, -, -, -}
+    // [ctas]: the pair that begins in this CTA and goes on in later ones: {last CTA (-1: no such
+    // pair), 2 * rows + slot of its part here, first flat row (token * group + head in group), key-value head}
     int4* join;
 };
 
-// Rows of a row tile (16, 32 or 64) and the head dimension's padded width.
+// Rows of a row tile (8, 32 or 64) and the head dimension's padded width.
 int kv_attention_rows(int group, int64_t max_new);
 int kv_attention_pad(int dim);
 struct KvAttnSpace {

@@ -181,14 +181,14 @@ template <typename TI, typename TC>
 cudaError_t launch_lanes(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream) {
     const int runs = a.cache.dim / 8, G = runs <= 8 ? 8 : runs <= 16 ? 16 : 32;
     const int heads = (a.q_out ? a.q_heads : 0) + 2 * a.cache.heads;
-    auto kern = G == 8 ? kv_append_kernel<TI, TC, 8> : G == 16 ? kv_append_kernel<TI, TC, 16> : kv_append_kernel<TI, TC, 32>;
-    cudaError_t e = set_max_carveout(kern);
-    if (e != cudaSuccess) return e;
     const int per_cta = (32 / G) * (kAppendThreads / 32);
     // few tokens: their heads spread over more CTAs
     const unsigned y = static_cast<unsigned>(a.step.tokens < sm_count ? cdiv(heads, per_cta) : 1);
     const unsigned x = static_cast<unsigned>(std::min<int64_t>(a.step.tokens, int64_t(sm_count) * 64));
-    return launch_ex(kern, dim3(x, y), dim3(kAppendThreads), 0, stream, pdl, a);
+    const dim3 grid(x, y), block(kAppendThreads);
+    if (G == 8) return launch_ready<kv_append_kernel<TI, TC, 8>>(grid, block, 0, stream, pdl, a);
+    if (G == 16) return launch_ready<kv_append_kernel<TI, TC, 16>>(grid, block, 0, stream, pdl, a);
+    return launch_ready<kv_append_kernel<TI, TC, 32>>(grid, block, 0, stream, pdl, a);
 }
 
 }  // namespace

@@ -22,32 +22,43 @@ MNB_SLICE_DECL(kv_attention_bf16_qf32)
 
 namespace {
 
-// One CTA per (CTA of the main kernel that begins a split pair, row of the
-// pair): out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts in
-// range order.  The parts are at most 2 MB in all and come from L2; the launch
-// and the two dependent loads (join record, then statistics) are what it costs.
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a split pair's parts in
+// range order.  One CTA per (CTA of the main kernel that begins a split pair, row
+// of the pair); its warps share the parts.  The parts come from L2 (2.5 MB in all
+// with 8-row tiles); what it costs is the launch and two dependent loads (the
+// record, then a warp's first parts together with the statistics), so it is kept
+// small: eight rows at a time in 256 threads took 2.4 us longer.
 template <int DP>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int rows_per_tile, int out_dtype) {
-    constexpr int NV = DP / 64;  // float2 per lane
+    constexpr int NV = DP / 64;    // float2 per lane
+    constexpr int AHEAD = 8 / NV;  // parts of a warp asked for before their weights are known
     __shared__ float weight[kKvMaxCtas];
     __shared__ float red[2][4];
     __shared__ float2 sums[4][32 * NV];
     grid_dependency_wait();
     grid_launch_dependents();
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 j = a.join[2 * c];
+    const int4 j = a.join[c];
     if (j.x < 0) return;
-    const int n = j.x - c + 1, head_kv = a.join[2 * c + 1].x;
-    for (int row = blockIdx.y; row < j.w; row += gridDim.y) {
-        auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + j.y : 2 * (c + i)) * rows_per_tile + row; };
+    const int n = j.x - c + 1, rows = j.y >> 1, slot0 = 2 * c + (j.y & 1), head_kv = j.w;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * rows_per_tile + row; };
+        auto o_at = [&](int i) { return reinterpret_cast<const float2*>(a.part_o + slot(i) * DP) + lane; };
         float m = -INFINITY;
         float2 ml[3];
 #pragma unroll
         for (int x = 0; x < 3; ++x) {  // kKvMaxCtas <= 3 * 128
             const int i = threadIdx.x + 128 * x;
             ml[x] = i < n ? a.part_ml[slot(i)] : make_float2(-INFINITY, 0.f);
-            m = fmaxf(m, ml[x].x);
         }
+        float2 ahead[AHEAD][NV];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                ahead[k][v] = warp + 4 * k < n ? o_at(warp + 4 * k)[v * 32] : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) m = fmaxf(m, ml[x].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) red[0][warp] = m;
@@ -70,13 +81,22 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
         float2 acc[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) acc[v] = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int i = warp; i < n; i += 4) {
-            const float w = weight[i];
-            const float2* o = reinterpret_cast<const float2*>(a.part_o + slot(i) * DP);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (warp + 4 * k >= n) break;
+            const float w = weight[warp + 4 * k];
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const float2 x = o[v * 32 + lane];
+                acc[v].x = fmaf(w, ahead[k][v].x, acc[v].x);
+                acc[v].y = fmaf(w, ahead[k][v].y, acc[v].y);
+            }
+        }
+#pragma unroll 4
+        for (int i = warp + 4 * AHEAD; i < n; i += 4) {
+            const float w = weight[i];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float2 x = o_at(i)[v * 32];
                 acc[v].x = fmaf(w, x.x, acc[v].x);
                 acc[v].y = fmaf(w, x.y, acc[v].y);
             }
@@ -84,8 +104,9 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
 #pragma unroll
         for (int v = 0; v < NV; ++v) sums[warp][v * 32 + lane] = acc[v];
         __syncthreads();
-        const int flat = j.z + row, head = head_kv * a.group + flat % a.group;
-        const int64_t token = flat / a.group;
+        const int flat = j.z + row, tok = a.by_group(flat);
+        const int64_t token = tok;
+        const int head = head_kv * a.group + flat - tok * a.group;
         if (threadIdx.x < 32 * NV) {
             const int d = threadIdx.x * 2;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
@@ -130,7 +151,7 @@ cudaError_t encode_cache(CUtensorMap* map, void* base, const KvCache& c, int box
 
 int kv_attention_rows(int group, int64_t max_new) {
     const int64_t rows = group * max_new;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 32 ? 32 : 64;
 }
 
 int kv_attention_pad(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -141,7 +162,7 @@ KvAttnSpace kv_attention_space(int rows, int pad) {
     s.part_o = 0;
     s.part_ml = up(s.part_o + int64_t(2) * kKvMaxCtas * rows * pad * 4);
     s.join = up(s.part_ml + int64_t(2) * kKvMaxCtas * rows * 8);
-    s.total = up(s.join + int64_t(2) * kKvMaxCtas * 16);
+    s.total = up(s.join + int64_t(kKvMaxCtas) * 16);
     return s;
 }
 
@@ -167,6 +188,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     a.part_o = reinterpret_cast<float*>(ws + sp.part_o);
     a.part_ml = reinterpret_cast<float2*>(ws + sp.part_ml);
     a.join = reinterpret_cast<int4*>(ws + sp.join);
+    a.by_group.set(static_cast<uint32_t>(a.group));
     // a TMA box holds as many rows as divide a page (at least 8, at most a tile)
     a.box_rows = kKvTile;
     while (a.cache.page_size % a.box_rows) a.box_rows >>= 1;
@@ -178,10 +200,10 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);
     int ctas = 0;
     if ((e = slice(kmap, vmap, a, rows, pad, sm_count, pdl, stream, &ctas)) != cudaSuccess) return e;
-    auto join = pad == 64 ? kv_join_kernel<64> : pad == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;
-    if ((e = set_max_carveout(join)) != cudaSuccess) return e;
-    const unsigned y = static_cast<unsigned>(std::min<int64_t>(rows, a.group * max_new));
-    return launch_ex(join, dim3(static_cast<unsigned>(ctas), y), dim3(128), 0, stream, pdl, a, rows, q_dtype);
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min<int64_t>(rows, a.group * max_new)));
+    if (pad == 64) return launch_ready<kv_join_kernel<64>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
+    if (pad == 128) return launch_ready<kv_join_kernel<128>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
+    return launch_ready<kv_join_kernel<256>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
 }
 
 }  // namespace mnb

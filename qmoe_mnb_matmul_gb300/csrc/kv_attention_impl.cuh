@@ -12,22 +12,26 @@
 // of a key-value head and the sequence's new tokens are the rows that share one
 // pass over its keys and values (row = token * group + head in group).  All
 // pairs' tiles form one line of units, cut into equal ranges, one per CTA (two
-// CTAs per SM, one where heads are wider than 128), so that one long sequence
-// or a ragged batch fills the GPU alike without the host knowing the lengths.  A pair that lies inside one range is written
-// out directly; the parts of a split pair go to the workspace (at most two per
-// CTA: the pair that began before the range, and the one that goes on after
-// it) and kv_join_kernel adds them in range order.
+// CTAs per SM, one where shared memory holds no more), so that one long sequence
+// or a ragged batch fills the GPU alike without the host knowing the lengths.
+// A pair that lies inside one range is written out directly; the parts of a
+// split pair go to the workspace (at most two per CTA: the pair that began
+// before the range, and the one that goes on after it) and kv_join_kernel adds
+// them in range order.
 //
-// Inside a CTA.  Warp 4 walks the units and loads tiles by TMA (4-D tensor map
-// over the cache's own strides, 128-byte swizzle, boxes of as many rows as
-// divide a page, page numbers from the page table) into a ring of slots that
-// hold a key tile or a value tile; rows past the sequence's end and page numbers
-// outside the cache read as zeros (an out-of-range box).  Warps 0-3 compute:
-// S = Q K^T and O += P V with mma.sync m16n8k16 (a decode step has 1 .. 64 rows;
-// it is bound by HBM, and the warp-level instructions need no accumulator
-// round trip through tensor memory), each warp a share of the tile's tokens
-// (16 rows or fewer: 16 tokens a warp) or of the rows (64 rows: 16 a warp).
-// Warps that share rows join through shared memory at the end of a pair.
+// Inside a CTA.  Warps 4 and 5 walk the units and load the key and the value
+// tiles by TMA (4-D tensor map over the cache's own strides, 128-byte swizzle,
+// boxes of as many rows as divide a page, page numbers from the page table) into
+// two rings of tiles; rows past the sequence's end and page numbers outside the
+// cache read as zeros (an out-of-range box).  Warps 0-3 compute, with the
+// tokens (and head dimensions) on the matrix instructions' long side and the
+// rows on their short one, in eights: S^T = K Q^T and O^T += V^T P^T by
+// mma.sync m16n8k16.  A step has 1 .. 64 rows and is bound by HBM: a decode
+// step of one to eight heads per key-value head wastes no more than it must of
+// an instruction, its accumulators stay in 32 registers, and nothing goes
+// through tensor memory and back.  The four warps split into WR groups along the
+// rows (8 RG rows each) and 4 / WR along a tile's tokens; warps that share rows
+// join through shared memory at the end of a pair.
 //
 // Rounding.  K and V are exact 16-bit operands.  Queries of the cache's type go
 // in as they are; fp32 queries are scaled by a power of two per row and split
@@ -51,24 +55,36 @@ namespace mnb {
 namespace {
 
 constexpr int kComputeWarps = 4;
-constexpr int kThreads = 32 * (kComputeWarps + 1);
+constexpr int kThreads = 32 * (kComputeWarps + 2);  // and a producer of key tiles, and one of value tiles
 
-// Shared-memory plan of one instantiation.
-template <int DP, int WR, bool QF32, int PARTS_Q>
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// 16-bit parts of a query and of an attention weight.
+constexpr int query_parts(int dt, bool qf32) { return !qf32 ? 1 : dt == kBF16 ? 3 : 2; }
+constexpr int weight_parts(int dt, bool qf32) { return !qf32 ? 2 : dt == kBF16 ? 3 : 2; }
+
+// Shared-memory plan of an instantiation for row tiles of up to ROWS rows.
+template <int DP, int ROWS, bool QF32, int PARTS_Q>
 struct Plan {
-    static constexpr int kRows = 16 * WR;
-    static constexpr int kTokenWarps = kComputeWarps / WR;
     static constexpr int kSlotBytes = kKvTile * DP * 2;
-    // Q parts (fp32 queries, and heads too wide to keep Q in registers)
-    static constexpr bool kQSmem = QF32 || DP > 128;
-    static constexpr int kQBytes = kQSmem ? PARTS_Q * kRows * DP * 2 : 0;
-    static constexpr int kMergeBytes = (kTokenWarps - 1) * kRows * DP * 4;
-    static constexpr int kCtasPerSm = DP > 128 ? 1 : 2;
-    // 227 KB a SM, 1 KB of it reserved per CTA, 2 KB for barriers, row statistics and alignment
-    static constexpr int kBudget = (kCtasPerSm == 2 ? 112 * 1024 : 226 * 1024) - 3072;
-    static constexpr int kFit = (kBudget - kQBytes - kMergeBytes) / kSlotBytes;
+    // Q parts (fp32 queries, and heads or row tiles too large to keep Q in registers)
+    static constexpr bool kQSmem = QF32 || DP > 128 || ROWS > 32;
+    static constexpr int kQBytes = kQSmem ? PARTS_Q * ROWS * DP * 2 : 0;
+    // join of the token warps: eight rows of half the columns per warp at a time,
+    // rows four words apart in the banks
+    static constexpr int kMergeRow = DP / 2 + 4;
+    static constexpr int kMergeBytes = kComputeWarps * 8 * kMergeRow * 4;
+    // 227 KB a SM, 1 KB of it reserved per CTA, 3 KB for barriers, row statistics and alignment
+    static constexpr int kRoom2 = 112 * 1024 - 3072 - kQBytes - kMergeBytes;
+    static constexpr int kRoom1 = 226 * 1024 - 3072 - kQBytes - kMergeBytes;
+    static constexpr int kCtasPerSm = DP <= 128 && kRoom2 >= 4 * kSlotBytes ? 2 : 1;
+    static constexpr int kFit = (kCtasPerSm == 2 ? kRoom2 : kRoom1) / kSlotBytes;
     static constexpr int kSlots = kFit > 8 ? 8 : kFit;
-    static constexpr int kBytes = 1024 + kSlots * kSlotBytes + kQBytes + kMergeBytes + 1024;
+    static constexpr int kKSlots = (kSlots + 1) / 2, kVSlots = kSlots / 2;  // of key tiles, of value tiles
+    static constexpr int kBytes = 1024 + kSlots * kSlotBytes + kQBytes + kMergeBytes;
     static_assert(kSlots >= 2, "a key tile and a value tile must fit");
 };
 
@@ -81,9 +97,9 @@ template <> struct Half2<kF16> {
     static __device__ __forceinline__ float2 unpack(uint32_t x) {
         return __half22float2(*reinterpret_cast<const __half2*>(&x));
     }
-    // whether either value is infinite or NaN
-    static __device__ __forceinline__ bool odd(uint32_t x) {
-        return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
+    // bits of the values of the pair that are infinite or NaN
+    static __device__ __forceinline__ uint32_t odd(uint32_t x) {
+        return ((x & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
     }
 };
 template <> struct Half2<kBF16> {
@@ -94,8 +110,8 @@ template <> struct Half2<kBF16> {
     static __device__ __forceinline__ float2 unpack(uint32_t x) {
         return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ bool odd(uint32_t x) {
-        return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+    static __device__ __forceinline__ uint32_t odd(uint32_t x) {
+        return ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
     }
 };
 
@@ -139,10 +155,24 @@ __device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values held one pair per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// A load that is issued where it stands (the compiler would move it to its use).
+__device__ __forceinline__ int load_now(const int* p) {
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
@@ -170,7 +200,8 @@ struct RowTile {
     int rows;       // rows in use
     int lo, hi;     // cached tokens that some row sees: [lo, hi)
     int lo_all, hi_all;  // cached tokens that every row sees: [lo_all, hi_all)
-    int tiles;      // units per key-value head, at least one
+    int tiles;      // per key-value head, at least one
+    int cost;       // units of a tile
 };
 
 struct Walk {
@@ -178,99 +209,48 @@ struct Walk {
     int rt, row_tiles;          // row tile, and how many the sequence has
     int h, tile;                // key-value head, next unit of the pair
     RowTile t;
-
-    template <int ROWS>
-    __device__ __forceinline__ static RowTile row_tile(const KvAttnArgs& a, int count, int pos0, int rt) {
-        RowTile t;
-        const int all = count * a.group;
-        t.first_row = rt * ROWS;
-        t.rows = min(ROWS, all - t.first_row);
-        const int tok0 = t.first_row / a.group, tok1 = (t.first_row + t.rows - 1) / a.group;
-        const int cap = a.step.capacity;
-        t.hi = min(max(pos0 + tok1 + 1, 0), cap);
-        t.hi_all = min(max(pos0 + tok0 + 1, 0), cap);
-        t.lo = a.window > 0 ? max(0, pos0 + tok0 + 1 - a.window) : 0;
-        t.lo_all = a.window > 0 ? max(0, pos0 + tok1 + 1 - a.window) : 0;
-        t.tiles = t.hi > t.lo ? (t.hi + kKvTile - 1) / kKvTile - t.lo / kKvTile : 1;
-        return t;
-    }
-
-    template <int ROWS>
-    __device__ __forceinline__ void load(const KvAttnArgs& a, int seq) {
-        b = seq;
-        step_tokens(a.step, seq, &first, &count);
-        // a length beyond the page table is cut there (the append call records it)
-        const int len = min(__ldg(a.step.seq_lens + seq), a.step.capacity);
-        pos0 = max(len, 0) - count;
-        row_tiles = (count * a.group + ROWS - 1) / ROWS;
-    }
 };
 
 template <int ROWS>
-__device__ __forceinline__ int64_t sequence_units(const KvAttnArgs& a, int seq) {
-    Walk w;
-    w.load<ROWS>(a, seq);
-    int64_t n = 0;
-    for (int rt = 0; rt < w.row_tiles; ++rt) n += Walk::row_tile<ROWS>(a, w.count, w.pos0, rt).tiles;
-    return n * a.cache.heads;
+__device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int pos0, int rt) {
+    RowTile t;
+    const int all = count * a.group;
+    t.first_row = rt * ROWS;
+    t.rows = min(ROWS, all - t.first_row);
+    const int tok0 = a.by_group(t.first_row), tok1 = a.by_group(t.first_row + t.rows - 1);
+    const int cap = a.step.capacity;
+    t.hi = min(max(pos0 + tok1 + 1, 0), cap);
+    t.hi_all = min(max(pos0 + tok0 + 1, 0), cap);
+    t.lo = a.window > 0 ? max(0, pos0 + tok0 + 1 - a.window) : 0;
+    t.lo_all = a.window > 0 ? max(0, pos0 + tok1 + 1 - a.window) : 0;
+    // a tile of more than 32 rows takes about twice the time of one that HBM bounds
+    // (its matrix instructions bound it: measured 4900 against 2700 cycles)
+    t.cost = ROWS > 32 && t.rows > 32 ? 2 : 1;
+    t.tiles = t.hi > t.lo ? (t.hi + kKvTile - 1) / kKvTile - t.lo / kKvTile : 1;
+    return t;
 }
 
-// The CTA's range of units and the walk's start, worked out by each warp for
-// itself (lane l adds up the sequences l * c .. (l + 1) * c - 1).
-struct Range {
-    int64_t at, end, total;
-    int ctas;  // CTAs that have units
-};
-
+// New tokens and row tiles of a sequence.
 template <int ROWS>
-__device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
-    const int lane = threadIdx.x & 31;
-    const int batch = a.step.batch, per = (batch + 31) / 32;
-    const int s0 = min(lane * per, batch), s1 = min(s0 + per, batch);
-    int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += sequence_units<ROWS>(a, s);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+__device__ __forceinline__ void load_sequence(const KvAttnArgs& a, Walk& w, int seq) {
+    w.b = seq;
+    // a length beyond the page table is cut there (kv_append records it)
+    const int len = min(__ldg(a.step.seq_lens + seq), a.step.capacity);
+    step_tokens(a.step, seq, &w.first, &w.count);
+    w.pos0 = max(len, 0) - w.count;
+    w.row_tiles = (w.count * a.group + ROWS - 1) / ROWS;
+}
+
+// Units of the sequence in w over all its row tiles, for one key-value head.
+template <int ROWS>
+__device__ __forceinline__ int64_t sequence_units(const KvAttnArgs& a, const Walk& w) {
+    int64_t n = 0;
+#pragma unroll 1
+    for (int rt = 0; rt < w.row_tiles; ++rt) {
+        const RowTile t = row_tile<ROWS>(a, w.count, w.pos0, rt);
+        n += t.tiles * t.cost;
     }
-    Range r;
-    r.total = __shfl_sync(0xffffffffu, incl, 31);
-    r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), r.total));
-    const int c = blockIdx.x;
-    if (c >= r.ctas) {
-        r.at = r.end = 0;
-        return r;
-    }
-    r.at = r.total * c / r.ctas;
-    r.end = r.total * (c + 1) / r.ctas;
-    const bool owner = incl - mine <= r.at && r.at < incl;
-    int seq = 0;
-    int64_t off = 0;
-    if (owner) {
-        off = r.at - (incl - mine);
-        seq = s0;
-        for (;;) {
-            const int64_t n = sequence_units<ROWS>(a, seq);
-            if (off < n) break;
-            off -= n;
-            ++seq;
-        }
-    }
-    const int src = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
-    seq = __shfl_sync(0xffffffffu, seq, src);
-    off = __shfl_sync(0xffffffffu, off, src);
-    w.load<ROWS>(a, seq);
-    for (w.rt = 0;; ++w.rt) {
-        w.t = Walk::row_tile<ROWS>(a, w.count, w.pos0, w.rt);
-        const int64_t n = static_cast<int64_t>(w.t.tiles) * a.cache.heads;
-        if (off < n) break;
-        off -= n;
-    }
-    w.h = static_cast<int>(off / w.t.tiles);
-    w.tile = static_cast<int>(off % w.t.tiles);
-    return r;
+    return n;
 }
 
 // The next pair after a finished one (call only while units remain).
@@ -280,182 +260,301 @@ __device__ __forceinline__ void next_pair(const KvAttnArgs& a, Walk& w) {
     if (++w.h < a.cache.heads) return;
     w.h = 0;
     if (++w.rt >= w.row_tiles) {
+#pragma unroll 1
         do {
-            w.load<ROWS>(a, w.b + 1);
+            load_sequence<ROWS>(a, w, w.b + 1);
         } while (w.row_tiles == 0);
         w.rt = 0;
     }
-    w.t = Walk::row_tile<ROWS>(a, w.count, w.pos0, w.rt);
+    w.t = row_tile<ROWS>(a, w.count, w.pos0, w.rt);
+}
+
+// floor(total * c / ctas) for c <= ctas <= kKvMaxCtas, in 32 bits where that
+// holds the product (a 64-bit division costs as much as a load).
+__device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) {
+    if (total < (int64_t(1) << 32) / kKvMaxCtas)
+        return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
+    return total * c / ctas;
+}
+
+// The CTA's range of units.
+struct Range {
+    int64_t at, end, total;
+    int ctas;  // CTAs that have units
+};
+
+// The range and the walk's start, worked out by each warp for itself: the lanes
+// take 32 sequences at a time, once for the total and once (kept in registers
+// where 32 are all there are) to find the sequence that the range begins in.
+// The way from the launch to the first copy passes through here, so it is short
+// rather than general: one load of lengths, two 32-bit divisions.
+template <int ROWS>
+__device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
+    const int lane = threadIdx.x & 31, batch = a.step.batch;
+    Walk mine = {};
+    int64_t tiles = 0, incl = 0, before = 0;
+    Range r;
+    r.total = r.at = r.end = 0;
+    r.ctas = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int s0 = 0; s0 < batch; s0 += 32) {
+            if (pass == 0 || batch > 32) {
+                tiles = 0;
+                if (s0 + lane < batch) {
+                    load_sequence<ROWS>(a, mine, s0 + lane);
+                    tiles = sequence_units<ROWS>(a, mine);
+                }
+                incl = tiles;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+            }
+            const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+            if (pass == 0) {
+                r.total += all;
+            } else {
+                // units here are those of one head: a sequence's heads come one after the other
+                const int64_t begin = before + (incl - tiles) * a.cache.heads, end = before + incl * a.cache.heads;
+                const unsigned owner = __ballot_sync(0xffffffffu, begin <= r.at && r.at < end);
+                if (owner) {
+                    const int src = __ffs(owner) - 1;
+                    w.b = s0 + src;
+                    w.first = __shfl_sync(0xffffffffu, mine.first, src);
+                    w.count = __shfl_sync(0xffffffffu, mine.count, src);
+                    w.pos0 = __shfl_sync(0xffffffffu, mine.pos0, src);
+                    w.row_tiles = __shfl_sync(0xffffffffu, mine.row_tiles, src);
+                    int64_t off = r.at - __shfl_sync(0xffffffffu, begin, src);
+#pragma unroll 1
+                    for (w.rt = 0;; ++w.rt) {
+                        w.t = row_tile<ROWS>(a, w.count, w.pos0, w.rt);
+                        const int64_t n = static_cast<int64_t>(w.t.tiles) * w.t.cost * a.cache.heads;
+                        if (off < n) break;
+                        off -= n;
+                    }
+                    const int pair = w.t.tiles * w.t.cost;  // units of a pair: below 2^27
+                    if (off < (int64_t(1) << 31)) {
+                        w.h = static_cast<int>(off) / pair;
+                        w.tile = static_cast<int>(off) - w.h * pair;
+                    } else {
+                        w.h = static_cast<int>(off / pair);
+                        w.tile = static_cast<int>(off % pair);
+                    }
+                    if (ROWS > 32 && w.t.cost == 2) {
+                        // a tile belongs to the CTA that its first unit falls to
+                        r.at += w.tile & 1;
+                        w.tile = (w.tile + 1) >> 1;
+                        if (w.tile == w.t.tiles && r.at < r.end) next_pair<ROWS>(a, w);
+                    }
+                    return r;
+                }
+                before += all * a.cache.heads;
+            }
+        }
+        if (pass == 0) {
+            r.total *= a.cache.heads;
+            // a range holds a tile's first unit: as many units as the dearest tile has
+            r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), r.total / (ROWS > 32 ? 2 : 1)));
+            const int c = blockIdx.x;
+            if (r.total > 0 && r.ctas == 0) r.ctas = 1;
+            if (c >= r.ctas) return r;  // fewer units than CTAs
+            r.at = share(r.total, c, r.ctas);
+            r.end = share(r.total, c + 1, r.ctas);
+        }
+    }
+    r.end = r.at;  // not reached: the range begins in some sequence
+    return r;
 }
 
 // ------------------------------------------------------------- the kernel
 
-template <int DT, bool QF32, int DP, int WR>
-__global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
-    kv_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                        const KvAttnArgs a) {
-    constexpr int PQ = QF32 ? (DT == kBF16 ? 3 : 2) : 1;
-    constexpr int PP = QF32 ? (DT == kBF16 ? 3 : 2) : 2;
-    using P = Plan<DP, WR, QF32, PQ>;
-    constexpr int ROWS = P::kRows, WT = P::kTokenWarps, SLOTS = P::kSlots;
-    constexpr int NS = kKvTile / WT / 8;   // score column tiles of a warp
-    constexpr int KB = NS / 2;             // 16-token blocks of a warp
-    constexpr int NO = DP / 8;             // output column tiles
-    constexpr int NOWN = NO / WT;          // output column tiles a warp owns after the join of the token warps
-    constexpr int KS = DP / 16;
-    using H = Half2<DT>;
+// Tiles of the walk's pair that begin within the next `units`.
+template <int ROWS>
+__device__ __forceinline__ int part_tiles(const Walk& w, int64_t units) {
+    if (ROWS > 32 && w.t.cost == 2) units = (units + 1) >> 1;
+    return static_cast<int>(min(static_cast<int64_t>(w.t.tiles - w.tile), units));
+}
 
-    extern __shared__ uint8_t raw[];
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* qs = base + SLOTS * P::kSlotBytes;
-    float* merge = reinterpret_cast<float*>(qs + P::kQBytes);
-    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS];
-    __shared__ float2 stats[kComputeWarps][16];
-    __shared__ float row_unit[ROWS];
+// What the compute warps share.
+struct Smem {
+    uint8_t *k, *v;  // rings of tiles
+    uint8_t* q;
+    float* merge;
+    uint64_t *k_full, *k_empty, *v_full, *v_empty;
+    float2* stats;    // [4][16]: a warp's running maximum and sum of its rows
+    float2* rows;     // [64]: the rows' maximum and sum after the join
+    float* row_unit;  // [64]: power of two that a row of fp32 queries was scaled down by
+};
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kComputeWarps);
-        }
-        fence_barrier_init();
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
-    }
-    __syncthreads();
-    grid_dependency_wait();
-    grid_launch_dependents();
-
-    Walk w;
-    const Range r = find_range<ROWS>(a, w);
-    int64_t at = r.at;
-
-    if (warp == kComputeWarps) {
-        // ------------------------------------------------- tile producer
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        const int R = a.box_rows, blocks = kKvTile / R, ps = a.cache.page_size;
-        int slot = 0, issued = 0;
-        uint32_t parity = 1;  // of the wait for an empty slot: the first round passes at once
-        bool ok = true;
-        while (at < r.end && ok) {
-            const int nt = static_cast<int>(min(static_cast<int64_t>(w.t.tiles - w.tile), r.end - at));
-            const int* pages = a.step.page_table + w.b * a.step.table_stride;
-            const int tile0 = w.t.lo / kKvTile + w.tile;
-            // lane l looks up the page of row block l of each tile, one tile ahead
-            auto page_of = [&](int tile) {
-                const int tok = tile * kKvTile + lane * R;
-                int page = -1;
-                if (lane < blocks && tok < w.t.hi && tok + R > w.t.lo) {
-                    page = __ldg(pages + tok / ps);
-                    if (page < 0 || page >= a.cache.num_pages) record_error(MNB_ERR_CONTENT);
-                }
-                return page;
-            };
-            int page = page_of(tile0);
-            for (int i = 0; i < nt && ok; ++i) {
-                const int cur = page;
-                if (i + 1 < nt) page = page_of(tile0 + i + 1);
-                for (int kv = 0; kv < 2; ++kv) {
-                    ok = warp_wait(&empty[slot], parity);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], P::kSlotBytes);
-                    __syncwarp();
-                    const uint32_t dst = smem_u32(base + slot * P::kSlotBytes);
-                    for (int x0 = 0; x0 < blocks * (DP / 64); x0 += 32) {
-                        const int x = x0 + lane, blk = x % blocks, panel = x / blocks;
-                        const int pg = __shfl_sync(0xffffffffu, cur, blk);
-                        if (panel < DP / 64) {
-                            const int tok = (tile0 + i) * kKvTile + blk * R;
-                            tma_load_4d(dst + panel * (kKvTile * 128) + blk * R * 128, kv ? &vmap : &kmap, panel * 64,
-                                        tok % ps, w.h, pg, &full[slot]);
-                        }
-                    }
-                    ++issued;
-                    if (++slot == SLOTS) {
-                        slot = 0;
-                        parity ^= 1;
-                    }
-                }
-            }
-            at += nt;
-            w.tile += nt;
-            if (at < r.end) next_pair<ROWS>(a, w);
-        }
-        // no copy may be in flight when the CTA ends, whatever the compute warps
-        // waited for: see the copies of the last slots land
-        for (int n = max(0, issued - SLOTS); n < issued; ++n)
-            warp_wait(&full[n % SLOTS], static_cast<uint32_t>(n / SLOTS) & 1u);
-        return;
-    }
-
-    // --------------------------------------------------------- compute warps
-    const int wr = warp % WR, wt = warp / WR;
-    const int quad = lane >> 2, qc = lane & 3;
-    const float scale2 = a.scale * 1.4426950408889634f;  // scores in log2 units
+// Position in the ring of slots.
+template <int SLOTS>
+struct Ring {
     int slot = 0;
     uint32_t parity = 0;
-    // A wait that gave up (recorded in the error word) ends the waiting but not
-    // the walk: every warp still meets the others at each barrier.
-    bool ok = true;
-    int join_last = -1, join_slot = 0, join_row = 0, join_rows = 0, join_head = 0;
-
-    while (at < r.end) {
-        const int nt = static_cast<int>(min(static_cast<int64_t>(w.t.tiles - w.tile), r.end - at));
-        const bool whole = w.tile == 0 && nt == w.t.tiles;
-        // ---- queries of the 16 rows of this warp (flat rows first_row + 16 wr ..)
-        uint32_t qf[P::kQSmem ? 1 : KS][4];
-        float c0 = scale2, c1 = scale2;  // score to log2 units, rows quad and quad + 8
-        // visible tokens [lo, hi) of the two rows this lane holds scores of
-        int row_lo[2], row_hi[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int rr = wr * 16 + quad + 8 * x;
-            const int pos = w.pos0 + (w.t.first_row + rr) / a.group;
-            row_hi[x] = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
-            row_lo[x] = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == SLOTS) {
+            slot = 0;
+            parity ^= 1;
         }
-        const int dim = a.cache.dim;
-        auto q_at = [&](int rr) {  // element offset of row rr's query
-            const int flat = w.t.first_row + rr;
-            return (w.first + flat / a.group) * a.q_stride +
-                   static_cast<int64_t>(w.h * a.group + flat % a.group) * dim;
-        };
-        if constexpr (!P::kQSmem) {
-            const uint16_t* q = static_cast<const uint16_t*>(a.q);
-            const int ra = wr * 16 + quad, rb = ra + 8;
-            const uint16_t* qa = q + (ra < w.t.rows ? q_at(ra) : 0);
-            const uint16_t* qb = q + (rb < w.t.rows ? q_at(rb) : 0);
+    }
+};
+
+// Barrier of the WR warps of token group wt; true where any thread brought true.
+template <int WR>
+__device__ __forceinline__ bool tokens_or(int wt, bool x) {
+    if constexpr (WR == 1) {
+        return __any_sync(0xffffffffu, x);
+    } else {
+        uint32_t y;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+            "bar.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(y)
+            : "r"(2 + wt), "n"(32 * WR), "r"(x ? 1u : 0u)
+            : "memory");
+        return y != 0;
+    }
+}
+
+// The key or the value tiles of the CTA's range, by one warp.  Lane l issues the
+// box of row block l % blocks and 64-column panel l / blocks of every tile (32
+// boxes at most) and looks up its page itself, one tile ahead.  This warp's own
+// pace bounds how fast tiles can be asked for (a box costs some 80 cycles, a
+// hand-off between warps as much again), so keys and values have a producer
+// each and the loop has no division.
+template <int DP, int ROWS, int SLOTS>
+__device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* map, uint8_t* slots, uint64_t* full,
+                                        uint64_t* empty, Walk w, const Range& r) {
+    constexpr int kSlotBytes = kKvTile * DP * 2;
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int R = a.box_rows, blocks = kKvTile / R, ps = a.cache.page_size;
+    const int panel = lane / blocks, row0 = (lane % blocks) * R;
+    const int step_pages = kKvTile / ps, step_rows = kKvTile % ps;
+    const bool issues = panel < DP / 64;
+    const uint32_t dst = smem_u32(slots) + panel * (kKvTile * 128) + row0 * 128;
+    Ring<SLOTS> ring;
+    int issued = 0;
+    int64_t at = r.at;
+    bool ok = true, bad = false;
+    while (at < r.end && ok) {
+        const int nt = part_tiles<ROWS>(w, r.end - at);
+        int tok = (w.t.lo / kKvTile + w.tile) * kKvTile + row0;
+        // page and row of the box at token tok; boxes that no row sees are asked for
+        // outside the cache, which fills them with zeros and reads nothing
+        const int* at_page = a.step.page_table + w.b * a.step.table_stride + tok / ps;
+        int row = tok % ps;
+        auto wanted = [&] { return issues && tok < w.t.hi && tok + R > w.t.lo; };
+        int page = wanted() ? load_now(at_page) : -1;
+        for (int i = 0; i < nt; ++i) {
+            const int cur = page, cur_row = row;
+            const bool outside = wanted() && (cur < 0 || cur >= a.cache.num_pages);
+            tok += kKvTile;
+            row += step_rows;
+            at_page += step_pages;
+            if (row >= ps) {
+                row -= ps;
+                ++at_page;
+            }
+            page = i + 1 < nt && wanted() ? load_now(at_page) : -1;
+            if (ok) ok = warp_wait(&empty[ring.slot], ring.parity ^ 1);  // the first round passes at once
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[ring.slot], kSlotBytes);
+            __syncwarp();
+            if (issues) tma_load_4d(dst + ring.slot * kSlotBytes, map, panel * 64, cur_row, w.h, cur, &full[ring.slot]);
+            bad = bad || outside;
+            ++issued;
+            ring.next();
+        }
+        at += nt * w.t.cost;
+        w.tile += nt;
+        if (at < r.end) next_pair<ROWS>(a, w);
+    }
+    if (bad) record_error(MNB_ERR_CONTENT);  // a page number outside the cache: its tokens read as zeros
+    // no copy may be in flight when the CTA ends, whatever the compute warps
+    // waited for: see the copies of the last slots land
+    for (int n = max(0, issued - SLOTS); n < issued; ++n)
+        warp_wait(&full[n % SLOTS], static_cast<uint32_t>(n / SLOTS) & 1u);
+}
+
+// One pair's tiles w.tile .. w.tile + nt - 1 by the four compute warps, WR of them
+// along the rows (8 RG rows each) and 4 / WR along a tile's tokens; the result goes
+// to the output (`whole`) or to slot `part` of the workspace.
+template <int DT, bool QF32, int DP, int ROWS, int WR, int RG, int KSLOTS, int VSLOTS>
+__device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, const Walk& w, int nt, bool whole, int part,
+                                         Ring<KSLOTS>& kring, Ring<VSLOTS>& vring, bool& ok) {
+    constexpr int PQ = query_parts(DT, QF32), PP = weight_parts(DT, QF32);
+    using P = Plan<DP, ROWS, QF32, PQ>;
+    using H = Half2<DT>;
+    constexpr int WT = kComputeWarps / WR;
+    constexpr int TOK = kKvTile / WT;  // tokens of a warp in a tile
+    constexpr int MT = TOK / 16;       // 16-token blocks of a warp
+    constexpr int ND = DP / 16;        // 16-column blocks of the output
+    constexpr int KS = DP / 16;        // steps along the head dimension of a score
+    static_assert(8 * RG * WR <= ROWS, "the row groups lie within a row tile");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wr = warp % WR, wt = warp / WR;
+    const int quad = lane >> 2, qc = lane & 3;
+    const int dim = a.cache.dim;
+    const int row0 = wr * 8 * RG;  // the warp's first row of the row tile
+    const float scale2 = a.scale * 1.4426950408889634f;  // scores to log2 units
+
+    // ---- queries: lane holds columns 2 qc, 2 qc + 1 (+ 8) of row quad of each eight
+    uint32_t qf[P::kQSmem ? 1 : KS][P::kQSmem ? 1 : RG][2];
+    float c[RG][2];  // scores to log2 units, rows 2 qc and 2 qc + 1 of each eight
+#pragma unroll
+    for (int g = 0; g < RG; ++g) c[g][0] = c[g][1] = scale2;
+    auto q_at = [&](int rr) {  // element offset of row rr's query
+        const int flat = w.t.first_row + rr, tok = a.by_group(flat);
+        return (w.first + tok) * a.q_stride + static_cast<int64_t>(w.h * a.group + flat - tok * a.group) * dim;
+    };
+    if constexpr (!P::kQSmem) {
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            const int rr = row0 + g * 8 + quad;
+            const bool in = rr < w.t.rows;
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + (in ? q_at(rr) : 0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int d = ks * 16 + x * 8 + qc * 2;
-                    qf[ks][2 * x] = ra < w.t.rows && d < dim ? __ldg(reinterpret_cast<const unsigned*>(qa + d)) : 0u;
-                    qf[ks][2 * x + 1] = rb < w.t.rows && d < dim ? __ldg(reinterpret_cast<const unsigned*>(qb + d)) : 0u;
+                    qf[ks][g][x] = in && d < dim ? __ldg(reinterpret_cast<const unsigned*>(q + d)) : 0u;
                 }
-        } else {
-            compute_sync();  // the queries of the pair before are read
-            // one warp per row in turn; fp32 rows are scaled to a largest magnitude in [1, 2)
-            for (int rr = warp; rr < ROWS; rr += kComputeWarps) {
-                constexpr int PL = (DP + 63) / 64;  // element pairs per lane
-                float2 v[PL];
-                float big = 0.f;
+        }
+    } else {
+        compute_sync();  // the queries of the pair before are read
+        if constexpr (QF32) {
+            // a warp takes every fourth row, several at a time so that their loads overlap;
+            // rows are scaled to a largest magnitude in [1, 2)
+            constexpr int PL = (DP + 63) / 64;  // element pairs per lane
+            constexpr int MINE = 2 * RG * WR, AT_ONCE = MINE < 4 ? MINE : 4;
+#pragma unroll 1
+            for (int k0 = 0; k0 < MINE; k0 += AT_ONCE) {
+                float2 v[AT_ONCE][PL];
 #pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    const int d = (i * 32 + lane) * 2;
-                    v[i] = make_float2(0.f, 0.f);
-                    if (rr < w.t.rows && d < dim) {
-                        if constexpr (QF32)
-                            v[i] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + q_at(rr) + d));
-                        else
-                            v[i] = H::unpack(__ldg(reinterpret_cast<const unsigned*>(
-                                static_cast<const uint16_t*>(a.q) + q_at(rr) + d)));
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const int rr = warp + (k0 + k) * kComputeWarps;
+                    const bool in = rr < w.t.rows;
+                    const int64_t at = in ? q_at(rr) : 0;
+#pragma unroll
+                    for (int i = 0; i < PL; ++i) {
+                        const int d = (i * 32 + lane) * 2;
+                        v[k][i] = make_float2(0.f, 0.f);
+                        if (in && d < dim)
+                            v[k][i] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + d));
                     }
-                    big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
                 }
-                float down = 1.f, up = 1.f;
-                if constexpr (QF32) {
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const int rr = warp + (k0 + k) * kComputeWarps;
+                    if (rr >= 8 * RG * WR) break;
+                    float down = 1.f, big = 0.f, up = 1.f;
+#pragma unroll
+                    for (int i = 0; i < PL; ++i) big = fmaxf(big, fmaxf(fabsf(v[k][i].x), fabsf(v[k][i].y)));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
                     // 2^-e and 2^e of the largest magnitude's exponent, for normal numbers
@@ -465,385 +564,498 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                         down = __uint_as_float((254u - e) << 23);
                         up = __uint_as_float(e << 23);
                     }
-                    if (lane == 0) row_unit[rr] = up;
-                }
+                    if (lane == 0) sm.row_unit[rr] = up;
 #pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    const int d = (i * 32 + lane) * 2;
-                    uint32_t part[PQ];
-                    split<DT, PQ>(v[i].x * down, v[i].y * down, part);
-#pragma unroll
-                    for (int p = 0; p < PQ; ++p)
-                        *reinterpret_cast<uint32_t*>(qs + p * (ROWS * DP * 2) + tile_at(ROWS, rr, d >> 3) +
-                                                     (d & 7) * 2) = part[p];
-                }
-            }
-            compute_sync();
-            if constexpr (QF32) {
-                c0 *= row_unit[wr * 16 + quad];
-                c1 *= row_unit[wr * 16 + quad + 8];
-            }
-        }
-
-        float o[NO][4];
-#pragma unroll
-        for (int n = 0; n < NO; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        const int tile0 = w.t.lo / kKvTile + w.tile;
-
-        for (int i = 0; i < nt; ++i) {
-            const int tok0 = (tile0 + i) * kKvTile + wt * (kKvTile / WT);  // the warp's first token
-            // tokens that not every row sees need a mask
-            const bool edge = tok0 < w.t.lo_all || tok0 + kKvTile / WT > w.t.hi_all;
-            // ---- scores
-            float s[NS][4];
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
-            if (ok) ok = warp_wait(&full[slot], parity);
-            {
-                const uint32_t kt = smem_u32(base + slot * P::kSlotBytes);
-                const int krow = wt * (kKvTile / WT) + (lane & 7) + ((lane >> 4) << 3), kchunk = (lane >> 3) & 1;
-                const uint32_t qt = smem_u32(qs);
-                const int qrow = wr * 16 + (lane & 15), qchunk = lane >> 4;
-                float rest[QF32 ? NS : 1][4];  // the smaller parts' products, added last
-                if constexpr (QF32) {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) rest[n][x] = 0.f;
-                }
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t qa[PQ][4];
-                    if constexpr (P::kQSmem) {
+                    for (int i = 0; i < PL; ++i) {
+                        const int d = (i * 32 + lane) * 2;
+                        uint32_t parts[PQ];
+                        split<DT, PQ>(v[k][i].x * down, v[k][i].y * down, parts);
 #pragma unroll
                         for (int p = 0; p < PQ; ++p)
-                            ldsm(qt + p * (ROWS * DP * 2) + tile_at(ROWS, qrow, ks * 2 + qchunk), qa[p]);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) qa[0][x] = qf[ks][x];
-                    }
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        uint32_t kf[4];
-                        ldsm(kt + tile_at(kKvTile, krow + kb * 16, ks * 2 + kchunk), kf);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            if constexpr (QF32) {
-                                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma<DT>(t, qa[0], kf[2 * n], kf[2 * n + 1]);
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) s[2 * kb + n][x] += t[x];
-#pragma unroll
-                                for (int p = 1; p < PQ; ++p) mma<DT>(rest[2 * kb + n], qa[p], kf[2 * n], kf[2 * n + 1]);
-                            } else {
-                                mma<DT>(s[2 * kb + n], qa[0], kf[2 * n], kf[2 * n + 1]);
-                            }
-                        }
+                            *reinterpret_cast<uint32_t*>(sm.q + p * (ROWS * DP * 2) + tile_at(ROWS, rr, d >> 3) + (d & 7) * 2) =
+                                parts[p];
                     }
                 }
-                if constexpr (QF32) {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) s[n][x] += rest[n][x];
-                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
-            if (++slot == SLOTS) {
-                slot = 0;
-                parity ^= 1;
+        } else {
+#pragma unroll 6
+            for (int x = threadIdx.x; x < 8 * RG * WR * (DP / 8); x += 32 * kComputeWarps) {
+                const int rr = x / (DP / 8), ch = x % (DP / 8);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < w.t.rows && ch * 8 < dim)
+                    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at(rr) + ch * 8));
+                *reinterpret_cast<uint4*>(sm.q + tile_at(ROWS, rr, ch)) = v;
             }
-            // ---- mask, running maximum and sum
-            if (edge) {
+        }
+        compute_sync();
+        if constexpr (QF32) {
 #pragma unroll
-                for (int n = 0; n < NS; ++n)
+            for (int g = 0; g < RG; ++g)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int j = tok0 + n * 8 + qc * 2 + (x & 1);
-                        if (j < row_lo[x >> 1] || j >= row_hi[x >> 1]) s[n][x] = -INFINITY;
-                    }
-            }
-            float b0 = m0, b1 = m1;
+                for (int x = 0; x < 2; ++x) c[g][x] *= sm.row_unit[row0 + g * 8 + qc * 2 + x];
+        }
+    }
+
+    float o[ND][RG][4];  // columns quad, quad + 8 of each sixteen; rows 2 qc, 2 qc + 1 of each eight
+    float m[RG][2], l[RG][2];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                b0 = fmaxf(b0, fmaxf(s[n][0], s[n][1]));
-                b1 = fmaxf(b1, fmaxf(s[n][2], s[n][3]));
-            }
+    for (int g = 0; g < RG; ++g) {
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1) {
-                b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, x));
-                b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, x));
-            }
-            // a row that has seen nothing yet keeps a zero reference, so that its exponentials are e^-inf = 0
-            const float r0 = b0 == -INFINITY ? 0.f : b0 * c0, r1 = b1 == -INFINITY ? 0.f : b1 * c1;
-            const float f0 = m0 == -INFINITY ? 0.f : exp2_approx(fmaf(m0, c0, -r0));
-            const float f1 = m1 == -INFINITY ? 0.f : exp2_approx(fmaf(m1, c1, -r1));
-            m0 = b0;
-            m1 = b1;
-            float t0 = 0.f, t1 = 0.f;
+        for (int n = 0; n < ND; ++n)
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                s[n][0] = exp2_approx(fmaf(s[n][0], c0, -r0));
-                s[n][1] = exp2_approx(fmaf(s[n][1], c0, -r0));
-                s[n][2] = exp2_approx(fmaf(s[n][2], c1, -r1));
-                s[n][3] = exp2_approx(fmaf(s[n][3], c1, -r1));
-                t0 += s[n][0] + s[n][1];
-                t1 += s[n][2] + s[n][3];
-            }
-            l0 = fmaf(l0, f0, t0);
-            l1 = fmaf(l1, f1, t1);
-            // ---- P in 16-bit parts, as the A operand of P V
-            uint32_t pf[KB][PP][4];
+            for (int x = 0; x < 4; ++x) o[n][g][x] = 0.f;
+        m[g][0] = m[g][1] = -INFINITY;
+        l[g][0] = l[g][1] = 0.f;
+    }
+    const bool active = row0 < w.t.rows;  // a warp whose rows are all padding only keeps the barriers
+    int tok0 = (w.t.lo / kKvTile + w.tile) * kKvTile + wt * TOK;  // the warp's first token
+    // This lane's ldmatrix row in a key tile, a value tile and Q.  The chunk's swizzle
+    // is an XOR of address bits 4 .. 6, so chunk c + 2 i of the row is the address of
+    // chunk c (0 or 1) XOR 32 i within a 128-byte panel.
+    const uint32_t k_lane = tile_at(kKvTile, wt * TOK + (lane & 15), lane >> 4);
+    const uint32_t v_lane = tile_at(kKvTile, wt * TOK + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    const uint32_t q_lane = smem_u32(sm.q) + tile_at(ROWS, row0 + (lane & 7), lane >> 3);
+    // tokens [lo, hi) that row `rr` of the row tile sees
+    auto sees = [&](int rr, int& lo, int& hi) {
+        const int pos = w.pos0 + a.by_group(w.t.first_row + rr);
+        hi = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
+        lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i, tok0 += kKvTile) {
+        // tokens that not every row sees
+        const bool edge = tok0 < w.t.lo_all || tok0 + TOK > w.t.hi_all;
+        // ---- scores.  With fp32 queries each product of the leading part starts from
+        // zero, is added outside, and the smaller parts are added last; otherwise two
+        // accumulators take turns along the head dimension where a warp has no other
+        // independent work (their chains are what a decode step waits for).
+        constexpr bool kTwo = !QF32 && MT * RG == 1;
+        float s[MT][RG][4], s2[QF32 || kTwo ? MT : 1][QF32 || kTwo ? RG : 1][4];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    uint32_t part[PP];
-                    split<DT, PP>(s[2 * kb + (x >> 1)][2 * (x & 1)], s[2 * kb + (x >> 1)][2 * (x & 1) + 1], part);
-#pragma unroll
-                    for (int p = 0; p < PP; ++p) pf[kb][p][x] = part[p];
+                    s[t][g][x] = 0.f;
+                    if constexpr (QF32 || kTwo) s2[t][g][x] = 0.f;
                 }
-            // ---- O = f O + P V
-            if (ok) ok = warp_wait(&full[slot], parity);
-            {
-                const uint32_t vt = smem_u32(base + slot * P::kSlotBytes);
-                const int vrow = wt * (kKvTile / WT) + (lane & 15), vchunk = lane >> 4;
+        if (ok) ok = warp_wait(&sm.k_full[kring.slot], kring.parity);
+        if (active) {
+            const uint32_t kt = smem_u32(sm.k + kring.slot * P::kSlotBytes) + k_lane;
 #pragma unroll
-                for (int n = 0; n < NO; n += 2) {
-                    float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            for (int kp = 0; kp < KS / 2; ++kp) {  // two steps along the head dimension
+                uint32_t qb[PQ][RG][4];
+                if constexpr (P::kQSmem) {
 #pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        uint32_t vf[4];
-                        ldsm_t(vt + tile_at(kKvTile, vrow + kb * 16, n + vchunk), vf);
-                        bool odd = false;
-                        if (edge) {
-                            // tokens no row sees: whatever the cache holds there counts as zero
+                    for (int p = 0; p < PQ; ++p)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const int j = tok0 + kb * 16 + (x & 1) * 8 + qc * 2;
-                                uint32_t keep = 0;
-                                if (j >= w.t.lo && j < w.t.hi) keep |= 0xFFFFu;
-                                if (j + 1 >= w.t.lo && j + 1 < w.t.hi) keep |= 0xFFFF0000u;
-                                vf[x] &= keep;
-                                odd = odd || H::odd(vf[x]);
-                            }
-                            odd = __any_sync(0xffffffffu, odd);
-                        }
-                        if (!odd) {
+                        for (int g = 0; g < RG; ++g)
+                            ldsm((q_lane ^ ((kp & 1) << 6)) + p * (ROWS * DP * 2) + (kp >> 1) * (ROWS * 128) + g * 1024,
+                                 qb[p][g]);
+                } else {
 #pragma unroll
-                            for (int p = PP - 1; p >= 0; --p) {
-                                mma<DT>(t[0], pf[kb][p], vf[0], vf[1]);
-                                mma<DT>(t[1], pf[kb][p], vf[2], vf[3]);
-                            }
-                        } else {
-                            // an infinity or a NaN among values that some rows see and others
-                            // do not: 0 * inf would reach the others, so each row adds only what
-                            // it sees (token e of the block is in lane e % 8 / 2 of the quad)
+                    for (int g = 0; g < RG; ++g)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int src = (lane & ~3) + ((e & 7) >> 1);
-                                float pa = 0.f, pb = 0.f;
+                        for (int x = 0; x < 4; ++x) qb[0][g][x] = qf[2 * kp + (x >> 1)][g][x & 1];
+                }
 #pragma unroll
-                                for (int p = PP - 1; p >= 0; --p) {
-                                    const float2 ua = H::unpack(__shfl_sync(0xffffffffu, pf[kb][p][2 * (e >> 3)], src));
-                                    const float2 ub = H::unpack(__shfl_sync(0xffffffffu, pf[kb][p][2 * (e >> 3) + 1], src));
-                                    pa += e & 1 ? ua.y : ua.x;
-                                    pb += e & 1 ? ub.y : ub.x;
-                                }
-                                const int j = tok0 + kb * 16 + e;
-                                const bool see_a = j >= row_lo[0] && j < row_hi[0];
-                                const bool see_b = j >= row_lo[1] && j < row_hi[1];
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const uint8_t* at_v = base + slot * P::kSlotBytes +
-                                                          tile_at(kKvTile, wt * (kKvTile / WT) + kb * 16 + e, n + y) + qc * 4;
-                                    const float2 v = H::unpack(*reinterpret_cast<const uint32_t*>(at_v));
-                                    if (see_a) {
-                                        t[y][0] = fmaf(pa, v.x, t[y][0]);
-                                        t[y][1] = fmaf(pa, v.y, t[y][1]);
-                                    }
-                                    if (see_b) {
-                                        t[y][2] = fmaf(pb, v.x, t[y][2]);
-                                        t[y][3] = fmaf(pb, v.y, t[y][3]);
-                                    }
-                                }
-                            }
-                        }
-                    }
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        o[n + y][0] = fmaf(o[n + y][0], f0, t[y][0]);
-                        o[n + y][1] = fmaf(o[n + y][1], f0, t[y][1]);
-                        o[n + y][2] = fmaf(o[n + y][2], f1, t[y][2]);
-                        o[n + y][3] = fmaf(o[n + y][3], f1, t[y][3]);
+                        const int ks = 2 * kp + y;
+                        uint32_t ka[4];
+                        ldsm((kt ^ ((ks & 3) << 5)) + (ks >> 2) * (kKvTile * 128) + t * 2048, ka);
+#pragma unroll
+                        for (int g = 0; g < RG; ++g) {
+                            if constexpr (QF32) {
+                                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma<DT>(z, ka, qb[0][g][2 * y], qb[0][g][2 * y + 1]);
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) s[t][g][x] += z[x];
+#pragma unroll
+                                for (int p = 1; p < PQ; ++p) mma<DT>(s2[t][g], ka, qb[p][g][2 * y], qb[p][g][2 * y + 1]);
+                            } else if constexpr (kTwo) {
+                                mma<DT>(y ? s2[t][g] : s[t][g], ka, qb[0][g][2 * y], qb[0][g][2 * y + 1]);
+                            } else {
+                                mma<DT>(s[t][g], ka, qb[0][g][2 * y], qb[0][g][2 * y + 1]);
+                            }
+                        }
                     }
+            }
+            if constexpr (QF32 || kTwo) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int g = 0; g < RG; ++g)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[t][g][x] += s2[t][g][x];
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_empty[kring.slot]);
+        kring.next();
+        // ---- mask, running maximum and sum.  s[t][g][x]: token 16 t + quad + 8 (x / 2), row 2 qc + x % 2
+        if (edge) {
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    int lo, hi;
+                    sees(row0 + g * 8 + qc * 2 + x, lo, hi);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j = tok0 + t * 16 + quad + 8 * y;
+                            if (j < lo || j >= hi) s[t][g][2 * y + x] = -INFINITY;
+                        }
                 }
+        }
+        float f[RG][2];
+        uint32_t pb[MT][RG][PP][2];  // P^T in 16-bit parts, as the B operand
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            float ref[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float big = m[g][x];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) big = fmaxf(big, fmaxf(s[t][g][x], s[t][g][2 + x]));
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
+                // a row that has seen nothing yet keeps a zero reference, so that its exponentials are 2^-inf = 0
+                ref[x] = big == -INFINITY ? 0.f : big * c[g][x];
+                f[g][x] = exp2_approx(fmaf(m[g][x], c[g][x], -ref[x]));
+                m[g][x] = big;
+            }
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[t][g][x] = exp2_approx(fmaf(s[t][g][x], c[g][x & 1], -ref[x & 1]));
+                    sum[x & 1] += s[t][g][x];
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t parts[PP];
+                    split<DT, PP>(s[t][g][2 * y], s[t][g][2 * y + 1], parts);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) pb[t][g][p][y] = transpose8(parts[p]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) l[g][x] = fmaf(l[g][x], f[g][x], sum[x]);
+        }
+        if (ok) ok = warp_wait(&sm.v_full[vring.slot], vring.parity);
+        uint8_t* vtile = sm.v + vring.slot * P::kSlotBytes;
+        if (edge) {
+            // What no row sees (past the sequence's end, before every window) counts as
+            // zero whatever the cache holds: the values are cleared in the tile.  An
+            // infinity or a NaN that some rows see must not reach the others as 0 * inf:
+            // it is cleared too once each row that sees it has added it (its weight, a
+            // positive number, changes nothing).
+            auto scan = [&](bool clear_odd) {
+                bool odd = false;
+#pragma unroll 1
+                for (int x = wr * 32 + lane; x < TOK * (DP / 8); x += 32 * WR) {
+                    const int e = x / (DP / 8), j = tok0 + e;
+                    uint4* at = reinterpret_cast<uint4*>(vtile + tile_at(kKvTile, wt * TOK + e, x % (DP / 8)));
+                    uint4 v = *at;
+                    const bool out = j < w.t.lo || j >= w.t.hi;
+                    uint32_t* y = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t bad = H::odd(y[k]);
+                        odd = odd || (bad != 0 && !out);
+                        y[k] = out ? 0u : y[k] & ~bad;
+                    }
+                    if (out || clear_odd) *at = v;
+                }
+                return odd;
+            };
+            if (tokens_or<WR>(wt, scan(false))) {
+                // O = f O + what each row sees of the infinities and NaNs
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    int lo[2], hi[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) sees(row0 + g * 8 + qc * 2 + x, lo[x], hi[x]);
+#pragma unroll
+                    for (int n = 0; n < ND; ++n) {
+                        float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                        for (int e = 0; e < TOK; ++e) {
+                            const int j = tok0 + e;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t v = *reinterpret_cast<const uint16_t*>(
+                                    vtile + tile_at(kKvTile, wt * TOK + e, 2 * n + y) + quad * 2);
+                                if (H::odd(v) == 0) continue;
+                                const float val = H::unpack(v).x;
+                                if (j >= lo[0] && j < hi[0]) add[2 * y] += val;
+                                if (j >= lo[1] && j < hi[1]) add[2 * y + 1] += val;
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[n][g][x] = fmaf(o[n][g][x], f[g][x & 1], add[x]);
+                    }
+                    f[g][0] = f[g][1] = 1.f;
+                }
+                tokens_or<WR>(wt, false);
+                scan(true);
+                tokens_or<WR>(wt, false);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
-            if (++slot == SLOTS) {
-                slot = 0;
-                parity ^= 1;
-            }
         }
-
-        // ---- end of the pair's part in this CTA
+        // ---- O^T = f O^T + V^T P^T
+        if (active) {
+            const uint32_t vt = smem_u32(vtile) + v_lane;
+            auto load_v = [&](int n, uint32_t (&va)[MT][4]) {
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-        }
-        // maxima to log2 units
-        m0 = m0 == -INFINITY ? m0 : m0 * c0;
-        m1 = m1 == -INFINITY ? m1 : m1 * c1;
-        if constexpr (WT > 1) {
-            // the token warps of a row group: common maximum and sum, then each
-            // warp adds up its share of the columns, in warp order
-            if (qc == 0) {
-                stats[warp][quad] = make_float2(m0, l0);
-                stats[warp][quad + 8] = make_float2(m1, l1);
-            }
-            compute_sync();
-            float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < WT; ++x) {
-                M0 = fmaxf(M0, stats[x * WR + wr][quad].x);
-                M1 = fmaxf(M1, stats[x * WR + wr][quad + 8].x);
-            }
-            const float R0 = M0 == -INFINITY ? 0.f : M0, R1 = M1 == -INFINITY ? 0.f : M1;
-            float L0 = 0.f, L1 = 0.f;
-#pragma unroll
-            for (int x = 0; x < WT; ++x) {
-                const float2 sa = stats[x * WR + wr][quad], sb = stats[x * WR + wr][quad + 8];
-                L0 = fmaf(sa.y, exp2_approx(sa.x - R0), L0);
-                L1 = fmaf(sb.y, exp2_approx(sb.x - R1), L1);
-            }
-            const float g0 = exp2_approx(m0 - R0), g1 = exp2_approx(m1 - R1);
-            m0 = M0;
-            m1 = M1;
-            l0 = L0;
-            l1 = L1;
-            // region of (row group, owner, source): 16 rows of DP / WT columns, 8-column groups swizzled by row
-            auto region = [&](int owner, int src) {
-                return merge + ((wr * WT + owner) * (WT - 1) + (src < owner ? src : src - 1)) * (16 * (DP / WT));
+                for (int t = 0; t < MT; ++t) ldsm_t((vt ^ ((n & 3) << 5)) + (n >> 2) * (kKvTile * 128) + t * 2048, va[t]);
             };
-            auto put = [&](int row, int n) { return row * (DP / WT) + (((n ^ row) & (NOWN - 1)) << 3) + qc * 2; };
+            // with one block of tokens the next sixteen columns are loaded ahead of the
+            // products of these (with more the registers do not allow it)
+            constexpr bool kAhead = MT == 1;
+            uint32_t va[2][MT][4];
+            if (kAhead) load_v(0, va[0]);
 #pragma unroll
-            for (int n = 0; n < NO; ++n) {
-                o[n][0] *= g0;
-                o[n][1] *= g0;
-                o[n][2] *= g1;
-                o[n][3] *= g1;
-                const int owner = n / NOWN;
-                if (owner != wt) {
-                    float* dst = region(owner, wt);
-                    *reinterpret_cast<float2*>(dst + put(quad, n)) = make_float2(o[n][0], o[n][1]);
-                    *reinterpret_cast<float2*>(dst + put(quad + 8, n)) = make_float2(o[n][2], o[n][3]);
-                }
-            }
-            compute_sync();
+            for (int n = 0; n < ND; ++n) {
+                if (!kAhead)
+                    load_v(n, va[n & 1]);
+                else if (n + 1 < ND)
+                    load_v(n + 1, va[(n + 1) & 1]);
+                float z[RG][4];
 #pragma unroll
-            for (int n = 0; n < NO; ++n) {
-                if (n / NOWN != wt) continue;
-                float2 sa = make_float2(0.f, 0.f), sb = sa;
+                for (int g = 0; g < RG; ++g)
 #pragma unroll
-                for (int x = 0; x < WT; ++x) {
-                    float2 va = make_float2(o[n][0], o[n][1]), vb = make_float2(o[n][2], o[n][3]);
-                    if (x != wt) {
-                        const float* from = region(wt, x);
-                        va = *reinterpret_cast<const float2*>(from + put(quad, n));
-                        vb = *reinterpret_cast<const float2*>(from + put(quad + 8, n));
-                    }
-                    sa.x += va.x;
-                    sa.y += va.y;
-                    sb.x += vb.x;
-                    sb.y += vb.y;
-                }
-                o[n][0] = sa.x;
-                o[n][1] = sa.y;
-                o[n][2] = sb.x;
-                o[n][3] = sb.y;
+                    for (int x = 0; x < 4; ++x) z[g][x] = 0.f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+                        for (int g = 0; g < RG; ++g) mma<DT>(z[g], va[n & 1][t], pb[t][g][p][0], pb[t][g][p][1]);
+#pragma unroll
+                for (int g = 0; g < RG; ++g)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[n][g][x] = fmaf(o[n][g][x], f[g][x & 1], z[g][x]);
             }
         }
-        // ---- write the rows: the output, or this CTA's part of a split pair
-        const int part = 2 * blockIdx.x + (at == r.at ? 0 : 1);
+        if (edge) fence_proxy_async_smem();  // cleared values, before the slot's next copy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_empty[vring.slot]);
+        vring.next();
+    }
+
+    // ---- end of the pair's part in this CTA: the warps that share rows agree on
+    // their maximum (in log2 units) and sum, and scale to it
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int rr = wr * 16 + quad + 8 * x;
-            if (rr >= w.t.rows) continue;
-            const float m = x ? m1 : m0, l = x ? l1 : l0;
-            if (whole) {
-                const int flat = w.t.first_row + rr;
-                const int64_t token = w.first + flat / a.group;
-                const int head = w.h * a.group + flat % a.group;
-                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-                const int64_t off = token * a.out_stride + static_cast<int64_t>(head) * dim;
 #pragma unroll
-                for (int n = 0; n < NO; ++n) {
-                    const int d = n * 8 + qc * 2;
-                    if (n / NOWN != wt || d >= dim) continue;
-                    const float u = o[n][2 * x] * inv, v = o[n][2 * x + 1] * inv;
-                    if constexpr (QF32)
-                        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + off + d) = make_float2(u, v);
-                    else
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + off + d) = H::pack(u, v);
+            for (int y = 4; y < 32; y <<= 1) l[g][x] += __shfl_xor_sync(0xffffffffu, l[g][x], y);
+            m[g][x] *= c[g][x];
+            if (quad == 0) sm.stats[warp * 16 + g * 8 + qc * 2 + x] = make_float2(m[g][x], l[g][x]);
+        }
+    compute_sync();
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int rr = g * 8 + qc * 2 + x;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int y = 0; y < WT; ++y) M = fmaxf(M, sm.stats[(y * WR + wr) * 16 + rr].x);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int y = 0; y < WT; ++y) {
+                const float2 st = sm.stats[(y * WR + wr) * 16 + rr];
+                L = fmaf(st.y, exp2_approx(st.x - ref), L);
+            }
+            if (wt == 0 && quad == 0) sm.rows[row0 + rr] = make_float2(M, L);
+            const float k = exp2_approx(m[g][x] - ref);
+#pragma unroll
+            for (int n = 0; n < ND; ++n) {
+                o[n][g][x] *= k;
+                o[n][g][2 + x] *= k;
+            }
+        }
+    // ---- through shared memory, eight rows of each row group and half the columns
+    // at a time: the token warps' shares are added in warp order, and rows come out
+    // contiguous.  (Rolled loops: this runs once or twice in a launch, so that the
+    // fetch of its instructions counts.  Written from the accumulators, unrolled, it
+    // made a short call 0.5 us slower.)
+    constexpr int HALF = DP / 2, V4 = HALF / 4;
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (g + half) compute_sync();  // the last share is read
+            float* mine = sm.merge + warp * 8 * P::kMergeRow;
+#pragma unroll
+            for (int n = 0; n < ND / 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mine[(qc * 2 + (x & 1)) * P::kMergeRow + n * 16 + quad + 8 * (x >> 1)] = o[half * (ND / 2) + n][g][x];
+            compute_sync();
+#pragma unroll 1
+            for (int i = threadIdx.x; i < 8 * WR * V4; i += 32 * kComputeWarps) {
+                const int d4 = i % V4, r8 = i / V4 % 8, grp = i / (8 * V4);
+                const int rr = grp * 8 * RG + g * 8 + r8, d = half * HALF + d4 * 4;
+                if (rr >= w.t.rows) continue;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < WT; ++y) {
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        sm.merge + ((y * WR + grp) * 8 + r8) * P::kMergeRow + d4 * 4);
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
                 }
-                if (a.lse && wt == 0 && qc == 0)
-                    a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            } else {
-                float* po = a.part_o + (static_cast<int64_t>(part) * ROWS + rr) * DP;
-#pragma unroll
-                for (int n = 0; n < NO; ++n)
-                    if (n / NOWN == wt)
-                        *reinterpret_cast<float2*>(po + n * 8 + qc * 2) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
-                if (wt == 0 && qc == 0) a.part_ml[static_cast<int64_t>(part) * ROWS + rr] = make_float2(m, l);
+                const float2 ml = sm.rows[rr];
+                if (whole) {
+                    const int flat = w.t.first_row + rr, tok = a.by_group(flat);
+                    const int64_t token = w.first + tok;
+                    const int head = w.h * a.group + flat - tok * a.group;
+                    const float inv = ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);  // NaN stays NaN
+                    const int64_t off = token * a.out_stride + static_cast<int64_t>(head) * dim + d;
+                    if (d < dim) {
+                        if constexpr (QF32)
+                            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + off) =
+                                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+                        else
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + off) =
+                                make_uint2(H::pack(sum.x * inv, sum.y * inv), H::pack(sum.z * inv, sum.w * inv));
+                    }
+                    if (a.lse && d == 0)
+                        a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
+                            ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+                } else {
+                    const int64_t at = static_cast<int64_t>(part) * ROWS + rr;
+                    *reinterpret_cast<float4*>(a.part_o + at * DP + d) = sum;
+                    if (d == 0) a.part_ml[at] = ml;
+                }
+            }
+        }
+    compute_sync();  // the statistics are read
+}
+
+template <int DT, bool QF32, int DP, int ROWS>
+__global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT, QF32)>::kCtasPerSm)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const KvAttnArgs a) {
+    using P = Plan<DP, ROWS, QF32, query_parts(DT, QF32)>;
+    constexpr int KSLOTS = P::kKSlots, VSLOTS = P::kVSlots;
+
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t k_full[KSLOTS], k_empty[KSLOTS], v_full[VSLOTS], v_empty[VSLOTS];
+    __shared__ float2 stats[kComputeWarps * 16], rows[64];
+    __shared__ float row_unit[64];
+    uint8_t* q_smem = base + P::kSlots * P::kSlotBytes;
+    const Smem sm = {base,    base + KSLOTS * P::kSlotBytes,
+                     q_smem,  reinterpret_cast<float*>(q_smem + P::kQBytes),
+                     k_full,  k_empty,
+                     v_full,  v_empty,
+                     stats,   rows,
+                     row_unit};
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < KSLOTS; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], kComputeWarps);
+        }
+        for (int s = 0; s < VSLOTS; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], kComputeWarps);
+        }
+        fence_barrier_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    Walk w = {};
+    const Range r = find_range<ROWS>(a, w);
+    if (warp == kComputeWarps) {
+        produce<DP, ROWS, KSLOTS>(a, &kmap, sm.k, k_full, k_empty, w, r);
+        return;
+    }
+    if (warp > kComputeWarps) {
+        produce<DP, ROWS, VSLOTS>(a, &vmap, sm.v, v_full, v_empty, w, r);
+        return;
+    }
+
+    // --------------------------------------------------------- compute warps
+    int64_t at = r.at;
+    Ring<KSLOTS> kring;
+    Ring<VSLOTS> vring;
+    // A wait that gave up (recorded in the error word) ends the waiting but not
+    // the walk: every warp still meets the others at each barrier.
+    bool ok = true;
+    int4 join = make_int4(-1, 0, 0, 0);
+#pragma unroll 1
+    while (at < r.end) {
+        const int nt = part_tiles<ROWS>(w, r.end - at);
+        const bool whole = w.tile == 0 && nt == w.t.tiles;
+        const int slot = at == r.at ? 0 : 1, part = 2 * blockIdx.x + slot;  // (r.at is the first part's first unit)
+        // the warps split along the rows only as far as the pair's rows need
+        auto run = [&](auto wr, auto rg) {
+            run_part<DT, QF32, DP, ROWS, decltype(wr)::value, decltype(rg)::value>(a, sm, w, nt, whole, part, kring, vring,
+                                                                                  ok);
+        };
+        if (ROWS == 8 || w.t.rows <= 8) {
+            run(Int<1>{}, Int<1>{});
+        } else if constexpr (ROWS > 8) {
+            if (w.t.rows <= 16) {
+                run(Int<1>{}, Int<2>{});
+            } else if (ROWS == 32 || w.t.rows <= 32) {
+                run(Int<2>{}, Int<2>{});
+            } else if constexpr (ROWS > 32) {
+                run(Int<4>{}, Int<2>{});
             }
         }
         if (w.tile == 0 && !whole) {  // the pair begins here and goes on in the next CTAs
-            join_last = static_cast<int>(((at + w.t.tiles) * r.ctas - 1) / r.total);
-            join_slot = at == r.at ? 0 : 1;
-            join_row = w.first * a.group + w.t.first_row;
-            join_rows = w.t.rows;
-            join_head = w.h;
+            // the CTA of the pair's last tile: the largest c whose range starts at or before its first unit
+            join = make_int4(static_cast<int>(((at + (w.t.tiles - 1) * w.t.cost + 1) * r.ctas - 1) / r.total),
+                             2 * w.t.rows + slot,
+                             w.first * a.group + w.t.first_row, w.h);
         }
-        at += nt;
+        at += nt * w.t.cost;
         w.tile += nt;
         if (at < r.end) next_pair<ROWS>(a, w);
     }
-    if (warp == 0 && lane == 0) {
-        a.join[2 * blockIdx.x] = make_int4(join_last, join_slot, join_row, join_rows);
-        a.join[2 * blockIdx.x + 1] = make_int4(join_head, 0, 0, 0);
-    }
+    if (warp == 0 && lane == 0) a.join[blockIdx.x] = join;
 }
 
 // ------------------------------------------------------------- host side
 
 // Shared by the instantiations of one (cache type, query type) slice.
-template <int DT, bool QF32, int DP, int WR>
+template <int DT, bool QF32, int DP, int ROWS>
 cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvAttnArgs& a, int sm_count, bool pdl,
                        cudaStream_t stream, int* ctas) {
-    using P = Plan<DP, WR, QF32, QF32 ? (DT == kBF16 ? 3 : 2) : 1>;
-    auto kern = kv_attention_kernel<DT, QF32, DP, WR>;
-    cudaError_t e = set_kernel_smem(kern, P::kBytes);
-    if (e != cudaSuccess) return e;
+    using P = Plan<DP, ROWS, QF32, query_parts(DT, QF32)>;
     const int most = sm_count * P::kCtasPerSm;
     *ctas = most < kKvMaxCtas ? most : kKvMaxCtas;
-    return launch_ex(kern, dim3(static_cast<unsigned>(*ctas)), dim3(kThreads), P::kBytes, stream, pdl, kmap, vmap, a);
+    return launch_ready<kv_attention_kernel<DT, QF32, DP, ROWS>>(dim3(static_cast<unsigned>(*ctas)), dim3(kThreads),
+                                                                 P::kBytes, stream, pdl, kmap, vmap, a);
 }
 
 template <int DT, bool QF32, int DP>
 cudaError_t launch_rows(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvAttnArgs& a, int rows, int sm_count,
                         bool pdl, cudaStream_t stream, int* ctas) {
-    if (rows == 16) return launch_one<DT, QF32, DP, 1>(kmap, vmap, a, sm_count, pdl, stream, ctas);
-    if (rows == 32) return launch_one<DT, QF32, DP, 2>(kmap, vmap, a, sm_count, pdl, stream, ctas);
-    return launch_one<DT, QF32, DP, 4>(kmap, vmap, a, sm_count, pdl, stream, ctas);
+    if (rows == 8) return launch_one<DT, QF32, DP, 8>(kmap, vmap, a, sm_count, pdl, stream, ctas);
+    if (rows == 32) return launch_one<DT, QF32, DP, 32>(kmap, vmap, a, sm_count, pdl, stream, ctas);
+    return launch_one<DT, QF32, DP, 64>(kmap, vmap, a, sm_count, pdl, stream, ctas);
 }
 
 }  // namespace

@@ -125,8 +125,8 @@ def test_attention_workspace(lib):
     assert lib.kv_attention_workspace_size(16, 8, 128, 1, None) == INVALID
     assert size(16, 8, 128, 1) == OK and n.value > 0
     one = n.value
-    assert size(16, 8, 128, 8) == OK and n.value == one       # 16 rows
-    assert size(16, 8, 128, 9) == OK and n.value > one        # 18 rows
+    assert size(16, 8, 128, 4) == OK and n.value == one       # 8 rows
+    assert size(16, 8, 128, 5) == OK and n.value > one        # 10 rows
     assert size(16, 8, 128, 10 ** 6) == OK and n.value < 64 << 20
     assert size(15, 8, 128, 1) == INVALID
     assert size(16, 8, 128, 0) == INVALID
