@@ -128,15 +128,17 @@ def library_path() -> str:
 
 # ------------------------------------------------------------- marshalling
 
+_DTYPE_CODES = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.float16:
-        return F16
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _ptr(x):
@@ -408,7 +410,7 @@ def kv_cache(k, v) -> KvCacheDesc:
         raise ValueError("the head dimension must have unit stride")
     d = KvCacheDesc(_on_gpu(k, "k"), _on_gpu(v, "v"), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[2],
                     k.shape[1], k.shape[3], _dtype_code(k))
-    d.tensors = (k, v)  # kept alive with the descriptor
+    d.tensors, d.ref = (k, v), ctypes.byref(d)  # kept alive with the descriptor
     return d
 
 
@@ -430,7 +432,7 @@ def kv_step(seq_lens, page_table, new_start=None, tokens=None, max_new=1) -> KvS
     d = KvStepDesc(_packed(seq_lens, "seq_lens", torch.int32), _packed(new_start, "new_start", torch.int32),
                    _on_gpu(page_table, "page_table", torch.int32), stride, batch, tokens, max_new,
                    page_table.shape[1])
-    d.tensors = (seq_lens, new_start, page_table)
+    d.tensors, d.ref = (seq_lens, new_start, page_table), ctypes.byref(d)
     return d
 
 
@@ -441,20 +443,23 @@ def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e
     max_pos, rot_dim = (0, 0) if cos_sin is None else cos_sin.shape
     d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32), max_pos, rot_dim, int(bool(interleaved)),
                    _packed(q_norm, "q_norm", torch.float32), _packed(k_norm, "k_norm", torch.float32), eps)
-    d.tensors = (cos_sin, q_norm, k_norm)
+    d.tensors, d.ref = (cos_sin, q_norm, k_norm), ctypes.byref(d)
     return d
 
 
 def _token_rows(t, name, tokens, heads, dim):
     """Pointer and token stride of [tokens, heads, head_dim] rows (heads adjacent within a token)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != tokens or (heads is not None and shape[1] != heads) or shape[2] != dim:
-        raise ValueError(f"{name} must be [{tokens}, {heads or 'heads'}, {dim}], not {list(shape)}")
-    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], not {list(t.shape)}")
+    n, h, d = t.shape
+    token, head, one = t.stride()
+    if n != tokens or h != heads or d != dim:
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], not {list(t.shape)}")
+    if one != 1 or (head != dim and h > 1):
         raise ValueError(f"the heads of a token of {name} must be adjacent")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr(), (stride[0] if tokens > 1 else max(shape[1] * dim, 8))
+    return t.data_ptr(), (token if tokens > 1 else h * dim)  # the stride of one token is never used
 
 
 def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True):
@@ -468,7 +473,7 @@ def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True
     qs = os_ = heads = 0
     if q is not None:
         heads = q.shape[1]
-        qp, qs = _token_rows(q, "q", n, None, dim)
+        qp, qs = _token_rows(q, "q", n, heads, dim)
         if q_out is not None:
             op, os_ = _token_rows(q_out, "q_out", n, heads, dim)
             if q_out.dtype != q.dtype:
@@ -477,8 +482,8 @@ def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True
         raise ValueError("q_out needs q")
     if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise TypeError("q, k and v must have one dtype")
-    st = load_library().kv_append(ctypes.byref(cache), ctypes.byref(step), None if rope is None else ctypes.byref(rope),
-                                  qp, qs, heads, kp, ks, vp, vs, _dtype_code(k), op, os_, _stream(stream))
+    st = load_library().kv_append(cache.ref, step.ref, None if rope is None else rope.ref, qp, qs, heads, kp,
+                                  ks, vp, vs, _dtype_code(k), op, os_, _stream(stream))
     if check:
         _check(st, "kv_append")
     return st
@@ -495,7 +500,7 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
     """Attention of the step's new tokens q [tokens, q_heads, head_dim] over the cache into out (same shape and
     dtype); scale defaults to head_dim ** -0.5, lse (f32 [tokens, q_heads]) is optional."""
     n, dim, heads = step.tokens, cache.head_dim, q.shape[1]
-    qp, qs = _token_rows(q, "q", n, None, dim)
+    qp, qs = _token_rows(q, "q", n, heads, dim)
     op, os_ = _token_rows(out, "out", n, heads, dim)
     if out.dtype != q.dtype:
         raise TypeError("out must have q's dtype")
@@ -509,7 +514,7 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
         import torch
         workspace = torch.empty(kv_attention_workspace_size(heads, cache.kv_heads, dim, step.max_new),
                                 dtype=torch.uint8, device=q.device)
-    st = load_library().kv_attention(ctypes.byref(cache), ctypes.byref(step), qp, qs, heads, _dtype_code(q), op, os_,
+    st = load_library().kv_attention(cache.ref, step.ref, qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
                                      _packed(workspace, "workspace", None), workspace.nbytes, _stream(stream))
     if check:
@@ -523,15 +528,15 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
     (standing drafts, the drawn token, -1s) and accepted int32 [batch]."""
     import torch
     batch, rows, vocab = target.shape
-    f32, i32 = torch.float32, torch.int32
-    if draft is not None and draft.shape != (batch, rows - 1, vocab):
+    n, f32, i32 = rows - 1, torch.float32, torch.int32
+    if draft is not None and draft.shape != (batch, n, vocab):
         raise ValueError("draft must be [batch, n, vocab]")
-    if rows == 1:
+    if n == 0:
         draft = None  # nothing was drafted
     for t, name in ((target, "target"), (draft, "draft")):
         if t is not None and vocab > 1 and t.stride(2) != 1:
             raise ValueError(f"{name} must have unit stride along the vocabulary")
-    for t, shape, name in ((draft_tokens, (batch, rows - 1), "draft_tokens"), (uniforms, (batch, rows), "uniforms"),
+    for t, shape, name in ((draft_tokens, (batch, n), "draft_tokens"), (uniforms, (batch, rows), "uniforms"),
                            (tokens, (batch, rows), "tokens"), (accepted, (batch,), "accepted"),
                            (n_drafts, (batch,), "n_drafts")):
         if t is not None and t.shape != shape:
@@ -540,10 +545,10 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
     def strides(t, n):  # those of an extent of one are never used
         return (t.stride(0) if batch > 1 else n * vocab), (t.stride(1) if n > 1 else vocab)
     ts, tr = strides(target, rows)
-    ds, dr = (0, 0) if draft is None else strides(draft, rows - 1)
+    ds, dr = (0, 0) if draft is None else strides(draft, n)
     st = load_library().draft_verify(_on_gpu(target, "target", f32), ts, tr, _on_gpu(draft, "draft", f32), ds, dr,
                                      _packed(draft_tokens, "draft_tokens", i32), _packed(n_drafts, "n_drafts", i32),
-                                     _packed(uniforms, "uniforms", f32), batch, rows - 1, vocab,
+                                     _packed(uniforms, "uniforms", f32), batch, n, vocab,
                                      _packed(tokens, "tokens", i32), _packed(accepted, "accepted", i32),
                                      _stream(stream))
     if check:

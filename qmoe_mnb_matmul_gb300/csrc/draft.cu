@@ -19,7 +19,7 @@
 // vocabulary: one pass over the one or two rows that matter, bound by HBM for a
 // batch and by the chain of gather, pass, exchange and search for one sequence.
 // The warps' totals are exchanged through distributed shared memory, and the one
-// warp whose run holds the drawn point searches it (a kilobyte or so, from L2).
+// warp whose run holds the drawn point reads a quarter of it again, from L2.
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,7 +30,7 @@ namespace mnb {
 
 namespace {
 
-constexpr int kDraftThreads = 512;
+constexpr int kDraftThreads = 256;
 constexpr int kDraftWarps = kDraftThreads / 32;
 constexpr int kMaxCluster = 16;
 
@@ -68,12 +68,19 @@ struct Weights {
     int64_t skip;
     __device__ __forceinline__ uint64_t of(float x, float y, int64_t i) const {
         const float w = fminf(fmaxf(x - y, 0.f), 1.f);
-        return i == skip ? 0ull : static_cast<uint64_t>(w * 1099511627776.f);
+        // floor(2^40 w) from the bits of w = m 2^(e - 150), m of 24 bits: m shifted by e -
+        // 110 (at most 17).  Zero and subnormal numbers shift out.  (The conversion
+        // instruction to 64 bits runs at a small fraction of the integer rate: with
+        // it the 64-sequence case took 37 us.)
+        const uint32_t bits = __float_as_uint(w), m = (bits & 0x7FFFFFu) | 0x800000u;
+        const int up = static_cast<int>(bits >> 23) - 110;
+        const uint32_t lo = up >= 0 ? m << up : m >> min(-up, 31), hi = up >= 0 ? __funnelshift_l(m, 0u, up) : 0u;
+        return i == skip ? 0ull : (static_cast<uint64_t>(hi) << 32) | lo;
     }
 };
 
-// Weights of entries i .. i + 3 (those below `end`), entry i a multiple of four
-// from the rows' start; VEC: both rows may be read 16 bytes at a time.
+// Weights of entries i .. i + 3 (zero from `end` on), i a multiple of four; VEC: both
+// rows may be read 16 bytes at a time.
 template <bool VEC>
 __device__ __forceinline__ void four(const Weights& w, int64_t i, int64_t end, uint64_t (&out)[4]) {
     float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -96,55 +103,88 @@ __device__ __forceinline__ void four(const Weights& w, int64_t i, int64_t end, u
     for (int e = 0; e < 4; ++e) out[e] = w.of(x[e], y[e], i + e);
 }
 
+// This lane's share of the weights of [lo, hi), and what it had added up before each
+// quarter of the run's steps (128 entries a step): the search starts at a quarter.
 template <bool VEC>
-__device__ __forceinline__ uint64_t run_sum(const Weights& w, int64_t lo, int64_t hi) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint64_t run_sum(const Weights& w, int64_t lo, int64_t hi, int quarter, uint64_t (&marks)[3]) {
+    const int lane = threadIdx.x & 31, steps = static_cast<int>(cdiv<int64_t>(hi - lo, 128));
     uint64_t sum = 0;
+    marks[0] = marks[1] = marks[2] = 0;
 #pragma unroll 4
-    for (int64_t i = lo + lane * 4; i < hi; i += 128) {
+    for (int s = 0; s < steps; ++s) {
         uint64_t e[4];
-        four<VEC>(w, i, hi, e);
+        four<VEC>(w, lo + s * 128 + lane * 4, hi, e);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (s == (k + 1) * quarter) marks[k] = sum;
         sum += (e[0] + e[1]) + (e[2] + e[3]);
     }
-    return warp_sum64(sum);
+    // quarters that begin past the last step begin with everything
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if ((k + 1) * quarter >= steps) marks[k] = sum;
+    return sum;
 }
 
-// The smallest entry of [lo, hi) whose inclusive sum from lo exceeds `goal`
-// (there is one: the run's total does).
+// The smallest entry of [lo, hi) whose inclusive sum from lo exceeds `goal` (there is
+// one: the run's total does), given the marks of run_sum.
 template <bool VEC>
-__device__ __forceinline__ int64_t run_search(const Weights& w, int64_t lo, int64_t hi, uint64_t goal) {
+__device__ __forceinline__ int64_t run_search(const Weights& w, int64_t lo, int64_t hi, int quarter, uint64_t goal,
+                                              const uint64_t (&marks)[3]) {
     const int lane = threadIdx.x & 31;
-    uint64_t before = 0;
-    for (int64_t i0 = lo; i0 < hi; i0 += 128) {
-        const int64_t i = i0 + lane * 4;
-        uint64_t e[4];
-        four<VEC>(w, i, hi, e);
-        uint64_t incl = (e[0] + e[1]) + (e[2] + e[3]);
-        const uint64_t mine = incl;
+    uint64_t skip = 0;
+    int64_t at = lo;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+    for (int k = 0; k < 3; ++k) {
+        const uint64_t m = warp_sum64(marks[k]);
+        if (m <= goal) {
+            skip = m;
+            at = lo + static_cast<int64_t>(k + 1) * quarter * 128;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + incl > goal);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            int64_t at = i;
-            uint64_t sum = before + incl - mine;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                sum += e[k];
-                if (sum <= goal && at == i + k) ++at;
-            }
-            return __shfl_sync(0xffffffffu, at, src);
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return hi - 1;
+    goal -= skip;
+    constexpr int kAtOnce = 4;  // steps read together
+    for (; at < hi; at += kAtOnce * 128) {
+        uint64_t e[kAtOnce][4], mine[kAtOnce], all = 0;
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s) {
+            four<VEC>(w, at + s * 128 + lane * 4, hi, e[s]);
+            mine[s] = (e[s][0] + e[s][1]) + (e[s][2] + e[s][3]);
+            all += mine[s];
+        }
+        all = warp_sum64(all);
+        if (all <= goal) {
+            goal -= all;
+            continue;
+        }
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s) {
+            uint64_t incl = mine[s];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, incl > goal);
+            if (past) {
+                int k = 0;
+                uint64_t sum = incl - mine[s];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    sum += e[s][x];
+                    if (sum <= goal && k == x) ++k;
+                }
+                const int src = __ffs(past) - 1;
+                return at + s * 128 + src * 4 + __shfl_sync(0xffffffffu, k, src);
+            }
+            goal -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    return hi - 1;  // not reached
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kDraftThreads) draft_verify_kernel(const DraftArgs a) {
+__global__ void __launch_bounds__(kDraftThreads, 4) draft_verify_kernel(const DraftArgs a) {
     __shared__ uint64_t totals[2][kDraftWarps];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -191,12 +231,13 @@ __global__ void __launch_bounds__(kDraftThreads) draft_verify_kernel(const Draft
     const int64_t warps = int64_t(ctas) * kDraftWarps, mine = int64_t(rank) * kDraftWarps + warp;
     const int64_t run = cdiv<int64_t>(cdiv<int64_t>(a.vocab, warps), 128) * 128;
     const int64_t lo = min(mine * run, a.vocab), hi = min(lo + run, a.vocab);
-    uint64_t part[kMaxCluster * kDraftWarps / 32], total = 0;
+    const int quarter = static_cast<int>(cdiv<int64_t>(run / 128, 4));
+    uint64_t marks[3], part[kMaxCluster * kDraftWarps / 32], total = 0;
     // Where the weights that a fallen draft leaves are all zero (p <= q
     // everywhere), the second pass draws from p itself.
     int pass = 0;
     for (;; ++pass) {
-        const uint64_t sum = run_sum<VEC>(w, lo, hi);
+        const uint64_t sum = warp_sum64(run_sum<VEC>(w, lo, hi, quarter, marks));
         if (lane == 0) totals[pass][warp] = sum;
         cluster_arrive();
         cluster_wait();
@@ -231,7 +272,7 @@ __global__ void __launch_bounds__(kDraftThreads) draft_verify_kernel(const Draft
     }
     int* out = a.tokens + b * (a.drafts + 1);
     if (before <= goal && goal < before + own) {
-        const int64_t token = run_search<VEC>(w, lo, hi, goal - before);
+        const int64_t token = run_search<VEC>(w, lo, hi, quarter, goal - before, marks);
         if (lane == 0) out[count] = static_cast<int>(token);
     }
     if (rank == 0 && warp == 0) {

@@ -10,9 +10,14 @@
 // launch and three dependent loads (new_start, seq_lens, page_table) for one
 // token.  A group of G lanes (the power of two at or above dim / 8) holds one
 // head vector, 8 elements a lane as two runs of four: in the rotated part a run
-// and its partner run, so that a rotation needs no exchange between lanes; the
-// head's data are loaded before the chain of table lookups is waited for.
+// and its partner run, so that a rotation needs no exchange between lanes.  A
+// warp takes one token (or a share of its heads, where tokens are few): its
+// angles, times the norm's weights, stay in registers over the heads, and those
+// are read two steps at a time (four
+// spilled registers at four CTAs per SM and took 75 us instead of 56 for 16920
+// tokens of 32 heads).
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -24,24 +29,29 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 
+// Four elements as floats, and as loaded.
 struct Run4 {
     float x[4];
 };
-
 template <typename T>
-__device__ __forceinline__ Run4 load4(const T* p) {
-    Run4 r;
-    if constexpr (sizeof(T) == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        r.x[0] = v.x; r.x[1] = v.y; r.x[2] = v.z; r.x[3] = v.w;
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        T e[4];
-        *reinterpret_cast<uint2*>(e) = v;
+struct Raw4 {
+    using V = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+    V v;
+    __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const V*>(p)); }
+    __device__ __forceinline__ Run4 widen() const {
+        Run4 r;
+        alignas(16) T e[4];
+        *reinterpret_cast<V*>(e) = v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.x[i] = to_f32(e[i]);
+        return r;
     }
-    return r;
+};
+
+__device__ __forceinline__ Run4 load4(const float* p) {
+    Raw4<float> r;
+    r.load(p);
+    return r.widen();
 }
 
 __device__ __forceinline__ __half round_to(float x, __half*) { return __float2half_rn(x); }
@@ -52,7 +62,7 @@ __device__ __forceinline__ void store4(T* p, const Run4& r) {
     if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(p) = make_float4(r.x[0], r.x[1], r.x[2], r.x[3]);
     } else {
-        T e[4];
+        alignas(16) T e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = round_to(r.x[i], static_cast<T*>(nullptr));
         *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
@@ -74,121 +84,201 @@ __device__ __forceinline__ int sequence_of(const KvStep& s, int t) {
     return before < s.batch && __ldg(s.new_start + before) <= t ? before : -1;
 }
 
-template <typename TI, typename TC, int G>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendArgs a) {
+// What a lane does with its eight elements of every head of q or of k: the runs
+// (e, f) at offsets i0 and i1, element e_j paired with f_j, become inv * (e A - f B) and
+// inv * (f C + e D), where the norm's weights are folded into the angles (A = w_e cos,
+// B = w_f sin, C = w_f cos, D = w_e sin) and inv is the head's reciprocal norm.
+struct Turn {
+    float A[4], B[4], C[4], D[4];
+};
+
+// Heads h, h + kPer, .. below `end` of one token, G lanes each: normed, rotated and
+// rounded from `src` to `dst` (pointers to the lane's head h).
+template <bool INTER, int G, typename TI, typename TO>
+__device__ __forceinline__ void turn_heads(const TI* src, int64_t src_step, TO* dst, int64_t dst_step, int h, int end,
+                                           bool in, int i0, int i1, bool turns, bool norm, const Turn& c, float inv_dim,
+                                           float eps) {
+    constexpr int kPer = 32 / G, kAtOnce = 2;
+#pragma unroll 1
+    for (int h0 = h; h0 - static_cast<int>(threadIdx.x & 31) / G < end; h0 += kAtOnce * kPer) {
+        Raw4<TI> x[kAtOnce] = {}, y[kAtOnce] = {};
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s)
+            if (in && h0 + s * kPer < end) {
+                x[s].load(src + s * src_step + i0);
+                y[s].load(src + s * src_step + i1);
+            }
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s) {
+            Run4 e = x[s].widen(), f = y[s].widen();
+            if (INTER) {  // pairs (0, 1), (2, 3) of each run
+                const Run4 u = e, w = f;
+                e = {{u.x[0], u.x[2], w.x[0], w.x[2]}};
+                f = {{u.x[1], u.x[3], w.x[1], w.x[3]}};
+            }
+            float inv = 1.f;
+            if (norm) {
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ss = fmaf(e.x[i], e.x[i], fmaf(f.x[i], f.x[i], ss));
+#pragma unroll
+                for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                inv = rsqrtf(fmaf(ss, inv_dim, eps));
+            }
+            Run4 u, w;
+            if (turns) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u.x[i] = fmaf(e.x[i], c.A[i], -f.x[i] * c.B[i]);
+                    w.x[i] = fmaf(f.x[i], c.C[i], e.x[i] * c.D[i]);
+                }
+            } else {  // past the rotated part: A and C alone
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u.x[i] = e.x[i] * c.A[i];
+                    w.x[i] = f.x[i] * c.C[i];
+                }
+            }
+            if (norm) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u.x[i] *= inv;
+                    w.x[i] *= inv;
+                }
+            }
+            if (INTER) {
+                e = u;
+                f = w;
+                u = {{e.x[0], f.x[0], e.x[1], f.x[1]}};
+                w = {{e.x[2], f.x[2], e.x[3], f.x[3]}};
+            }
+            if (in && h0 + s * kPer < end) {
+                store4(dst + s * dst_step + i0, u);
+                store4(dst + s * dst_step + i1, w);
+            }
+        }
+        src += kAtOnce * src_step;
+        dst += kAtOnce * dst_step;
+    }
+}
+
+// blockIdx.x: eight tokens, one per warp; blockIdx.y: a share of `steps` steps of 32 /
+// G heads each, over the steps of q, then of k, then of v.
+template <typename TI, typename TC, int G, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const KvAppendArgs a, int steps) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane % G, dim = a.cache.dim, kv_heads = a.cache.heads;
-    const int first_k = a.q_heads, first_v = first_k + kv_heads, heads = first_v + kv_heads;
-    constexpr int kHeadsPerWarp = 32 / G, kHeadsPerCta = kHeadsPerWarp * (kAppendThreads / 32);
-    // the lane's runs: (i0, i1), a rotated pair where `turns`
+    const int lane = threadIdx.x & 31;
+    const int sub = lane % G, dim = a.cache.dim;
+    constexpr int kPer = 32 / G;  // heads per step
+    const int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (t >= a.step.tokens) return;
+    const int seq = sequence_of(a.step, t);
+    if (seq < 0) return;  // a token of no sequence
+    int first, count;
+    step_tokens(a.step, seq, &first, &count);
+    const int64_t pos = int64_t(__ldg(a.step.seq_lens + seq)) - count + (t - first);
+    if (pos < 0) return;  // a padding token: no position, nothing to write
+    // the lane's runs: (i0, i1), rotated pairs where `turns`
     const bool in = sub * 8 < dim;
     const int half = a.cos_sin ? a.rot_dim / 2 : 0;
     const bool turns = sub * 4 < half;
-    const bool apart = turns && !a.interleaved;
+    const bool apart = turns && !INTER;
     const int i0 = apart ? sub * 4 : sub * 8, i1 = apart ? half + sub * 4 : sub * 8 + 4;
+    const bool has_angle = a.cos_sin == nullptr || pos < a.max_pos;
+    Run4 cs = {{1.f, 1.f, 1.f, 1.f}}, sn = {};
+    if (turns && has_angle) {
+        const float* row = a.cos_sin + pos * a.rot_dim + sub * 4;
+        cs = load4(row);
+        sn = load4(row + half);
+    }
+    // (position < 2^31: seq_lens is 32-bit)
+    const int index = static_cast<int>(pos) / a.cache.page_size, row = static_cast<int>(pos) - index * a.cache.page_size;
+    int page = -1;
+    if (pos < a.step.capacity) page = __ldg(a.step.page_table + seq * a.step.table_stride + index);
+    if (!has_angle || page < 0 || page >= a.cache.num_pages) {
+        record_error(MNB_ERR_CONTENT);
+        return;
+    }
+    const int64_t slot = page * a.cache.page_stride + row * a.cache.token_stride;
+    const float inv_dim = 1.f / dim;
+    const int64_t src_step = kPer * dim, dst_step = kPer * a.cache.head_stride;
 
-    for (int64_t t = blockIdx.x; t < a.step.tokens; t += gridDim.x) {
-        const int seq = sequence_of(a.step, static_cast<int>(t));
-        if (seq < 0) continue;  // a token of no sequence
-        int first, count;
-        step_tokens(a.step, seq, &first, &count);
-        const int64_t pos = int64_t(__ldg(a.step.seq_lens + seq)) - count + (t - first);
-        if (pos < 0) continue;  // a padding token: no position, nothing to write
-        const bool has_slot = pos < a.step.capacity;
-        const bool has_angle = a.cos_sin == nullptr || pos < a.max_pos;
-        int page = -1;
-        if (has_slot) page = __ldg(a.step.page_table + seq * a.step.table_stride + pos / a.cache.page_size);
-        if (!has_angle || page < 0 || page >= a.cache.num_pages) {
-            record_error(MNB_ERR_CONTENT);
-            continue;
+    auto turn_of = [&](const float* weights) {
+        Run4 wu = {{1.f, 1.f, 1.f, 1.f}}, ww = wu;
+        if (weights != nullptr && in) {
+            wu = load4(weights + i0);
+            ww = load4(weights + i1);
         }
-        const int64_t slot = page * a.cache.page_stride + (pos % a.cache.page_size) * a.cache.token_stride;
-        Run4 cs, sn;
-        if (turns) {
-            const float* row = a.cos_sin + pos * a.rot_dim + sub * 4;
-            cs = load4(row);
-            sn = load4(row + half);
+        if (INTER) {
+            const Run4 u = wu, w = ww;
+            wu = {{u.x[0], u.x[2], w.x[0], w.x[2]}};
+            ww = {{u.x[1], u.x[3], w.x[1], w.x[3]}};
         }
-        for (int h0 = blockIdx.y * kHeadsPerCta + warp * kHeadsPerWarp; h0 < heads; h0 += gridDim.y * kHeadsPerCta) {
-            const int h = h0 + lane / G;
-            const bool live = in && h < heads && (h >= first_k || a.q_out != nullptr);
-            const TI* src;
-            if (h < first_k)
-                src = static_cast<const TI*>(a.q) + t * a.q_stride + int64_t(h) * dim;
-            else if (h < first_v)
-                src = static_cast<const TI*>(a.k) + t * a.k_stride + int64_t(h - first_k) * dim;
-            else
-                src = static_cast<const TI*>(a.v) + t * a.v_stride + int64_t(h - first_v) * dim;
-            Run4 u = {}, v = {};
-            if (live) {
-                u = load4(src + i0);
-                v = load4(src + i1);
-            }
-            const float* w = h < first_k ? a.q_norm : h < first_v ? a.k_norm : nullptr;
-            float ss = 0.f;
+        Turn c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ss = fmaf(u.x[i], u.x[i], fmaf(v.x[i], v.x[i], ss));
-#pragma unroll
-            for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (!live) continue;
-            if (w != nullptr) {
-                const float inv = 1.f / sqrtf(ss / dim + a.eps);
-                const Run4 wu = load4(w + i0), wv = load4(w + i1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u.x[i] = u.x[i] * inv * wu.x[i];
-                    v.x[i] = v.x[i] * inv * wv.x[i];
-                }
-            }
-            if (turns && h < first_v) {
-                if (a.interleaved) {  // pairs (u0, u1), (u2, u3), (v0, v1), (v2, v3)
-                    Run4 x = u, y = v;
-                    u.x[0] = x.x[0] * cs.x[0] - x.x[1] * sn.x[0];
-                    u.x[1] = x.x[1] * cs.x[0] + x.x[0] * sn.x[0];
-                    u.x[2] = x.x[2] * cs.x[1] - x.x[3] * sn.x[1];
-                    u.x[3] = x.x[3] * cs.x[1] + x.x[2] * sn.x[1];
-                    v.x[0] = y.x[0] * cs.x[2] - y.x[1] * sn.x[2];
-                    v.x[1] = y.x[1] * cs.x[2] + y.x[0] * sn.x[2];
-                    v.x[2] = y.x[2] * cs.x[3] - y.x[3] * sn.x[3];
-                    v.x[3] = y.x[3] * cs.x[3] + y.x[2] * sn.x[3];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = u.x[i], y = v.x[i];
-                        u.x[i] = x * cs.x[i] - y * sn.x[i];
-                        v.x[i] = y * cs.x[i] + x * sn.x[i];
-                    }
-                }
-            }
-            if (h < first_k) {
-                TI* dst = static_cast<TI*>(a.q_out) + t * a.q_out_stride + int64_t(h) * dim;
-                store4(dst + i0, u);
-                store4(dst + i1, v);
-            } else {
-                const bool is_k = h < first_v;
-                TC* dst = static_cast<TC*>(is_k ? a.cache.k : a.cache.v) + slot +
-                          (h - (is_k ? first_k : first_v)) * a.cache.head_stride;
-                store4(dst + i0, u);
-                store4(dst + i1, v);
-            }
+        for (int i = 0; i < 4; ++i) {
+            c.A[i] = wu.x[i] * cs.x[i];
+            c.B[i] = ww.x[i] * sn.x[i];
+            c.C[i] = ww.x[i] * cs.x[i];
+            c.D[i] = wu.x[i] * sn.x[i];
+        }
+        return c;
+    };
+    // this share's steps, section by section
+    const int q_steps = a.q_out ? cdiv(a.q_heads, kPer) : 0, kv_steps = cdiv(a.cache.heads, kPer);
+    const int s0 = blockIdx.y * steps, s1 = s0 + steps;
+    const int group = lane / G;
+    auto section = [&](int before, int n, int heads, int* begin, int* end) {  // heads [begin, end) of a section
+        *begin = max(s0 - before, 0) * kPer;
+        *end = min(min(s1 - before, n) * kPer, heads);
+        return *begin < *end;
+    };
+    int begin, end;
+    if (section(0, q_steps, a.q_heads, &begin, &end)) {
+        const int64_t at = int64_t(begin + group) * dim;
+        turn_heads<INTER, G>(static_cast<const TI*>(a.q) + t * a.q_stride + at, src_step,
+                             static_cast<TI*>(a.q_out) + t * a.q_out_stride + at, src_step, begin + group, end, in, i0, i1,
+                             turns, a.q_norm != nullptr, turn_of(a.q_norm), inv_dim, a.eps);
+    }
+    if (section(q_steps, kv_steps, a.cache.heads, &begin, &end)) {
+        turn_heads<INTER, G>(static_cast<const TI*>(a.k) + t * a.k_stride + int64_t(begin + group) * dim, src_step,
+                             static_cast<TC*>(a.cache.k) + slot + (begin + group) * a.cache.head_stride, dst_step,
+                             begin + group, end, in, i0, i1, turns, a.k_norm != nullptr, turn_of(a.k_norm), inv_dim, a.eps);
+    }
+    if (section(q_steps + kv_steps, kv_steps, a.cache.heads, &begin, &end) && in) {
+        const TI* src = static_cast<const TI*>(a.v) + t * a.v_stride + int64_t(begin + group) * dim + sub * 8;
+        TC* dst = static_cast<TC*>(a.cache.v) + slot + (begin + group) * a.cache.head_stride + sub * 8;
+#pragma unroll 4
+        for (int h = begin + group; h < end; h += kPer, src += src_step, dst += dst_step) {
+            Raw4<TI> x, y;
+            x.load(src);
+            y.load(src + 4);
+            store4(dst, x.widen());
+            store4(dst + 4, y.widen());
         }
     }
 }
 
+template <typename TI, typename TC, int G>
+cudaError_t launch_group(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream) {
+    // A token's heads are shared by as many warps as give every SM about 12 (one head
+    // step each at most; with 24 the steps of 200 tokens took 4.6 us instead of 3.9):
+    // few tokens are bound by latency, many by HBM.
+    const int all = (a.q_out ? cdiv(a.q_heads, 32 / G) : 0) + 2 * cdiv(a.cache.heads, 32 / G);
+    const int64_t want = cdiv<int64_t>(int64_t(sm_count) * 12, a.step.tokens);
+    const int steps = cdiv(all, static_cast<int>(std::min<int64_t>(want, all)));
+    const dim3 grid(static_cast<unsigned>(cdiv(a.step.tokens, kAppendThreads / 32)), static_cast<unsigned>(cdiv(all, steps)));
+    if (a.interleaved)
+        return launch_ready<kv_append_kernel<TI, TC, G, true>>(grid, dim3(kAppendThreads), 0, stream, pdl, a, steps);
+    return launch_ready<kv_append_kernel<TI, TC, G, false>>(grid, dim3(kAppendThreads), 0, stream, pdl, a, steps);
+}
+
 template <typename TI, typename TC>
 cudaError_t launch_lanes(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream) {
-    const int runs = a.cache.dim / 8, G = runs <= 8 ? 8 : runs <= 16 ? 16 : 32;
-    const int heads = (a.q_out ? a.q_heads : 0) + 2 * a.cache.heads;
-    const int per_cta = (32 / G) * (kAppendThreads / 32);
-    // few tokens: their heads spread over more CTAs
-    const unsigned y = static_cast<unsigned>(a.step.tokens < sm_count ? cdiv(heads, per_cta) : 1);
-    const unsigned x = static_cast<unsigned>(std::min<int64_t>(a.step.tokens, int64_t(sm_count) * 64));
-    const dim3 grid(x, y), block(kAppendThreads);
-    if (G == 8) return launch_ready<kv_append_kernel<TI, TC, 8>>(grid, block, 0, stream, pdl, a);
-    if (G == 16) return launch_ready<kv_append_kernel<TI, TC, 16>>(grid, block, 0, stream, pdl, a);
-    return launch_ready<kv_append_kernel<TI, TC, 32>>(grid, block, 0, stream, pdl, a);
+    if (a.cache.dim <= 64) return launch_group<TI, TC, 8>(a, sm_count, pdl, stream);
+    if (a.cache.dim <= 128) return launch_group<TI, TC, 16>(a, sm_count, pdl, stream);
+    return launch_group<TI, TC, 32>(a, sm_count, pdl, stream);
 }
 
 }  // namespace
