@@ -19,7 +19,7 @@
 // vocabulary: one pass over the one or two rows that matter, bound by HBM for a
 // batch and by the chain of gather, pass, exchange and search for one sequence.
 // The warps' totals are exchanged through distributed shared memory, and the one
-// warp whose run holds the drawn point reads a quarter of it again, from L2.
+// warp whose run holds the drawn point reads half of it again, from L2.
 #include <algorithm>
 
 #include "common.cuh"
@@ -61,29 +61,37 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 }
 
 // The row whose weights are drawn from: max(p - q, 0) in units of 2^-40, q null
-// for p itself, entry `skip` left out.  (fmaxf drops a NaN.)
+// for p itself, entry `skip` left out (-1: none).
 struct Weights {
     const float* p;
     const float* q;
-    int64_t skip;
-    __device__ __forceinline__ uint64_t of(float x, float y, int64_t i) const {
-        const float w = fminf(fmaxf(x - y, 0.f), 1.f);
-        // floor(2^40 w) from the bits of w = m 2^(e - 150), m of 24 bits: m shifted by e -
-        // 110 (at most 17).  Zero and subnormal numbers shift out.  (The conversion
-        // instruction to 64 bits runs at a small fraction of the integer rate: with
-        // it the 64-sequence case took 37 us.)
-        const uint32_t bits = __float_as_uint(w), m = (bits & 0x7FFFFFu) | 0x800000u;
-        const int up = static_cast<int>(bits >> 23) - 110;
-        const uint32_t lo = up >= 0 ? m << up : m >> min(-up, 31), hi = up >= 0 ? __funnelshift_l(m, 0u, up) : 0u;
-        return i == skip ? 0ull : (static_cast<uint64_t>(hi) << 32) | lo;
-    }
+    int skip;
 };
 
-// Weights of entries i .. i + 3 (zero from `end` on), i a multiple of four; VEC: both
+// floor(2^40 w) of w = min(max(x, 0), 1) (fmaxf drops a NaN), in two parts of 20 bits:
+// adding 8 to w with rounding toward zero leaves floor(2^20 w) in the sum's low
+// bits, and adding 2^-17 to what that cut off leaves the next 20 bits likewise.  Both
+// parts still carry the bits of the number added (kHi, kLo), taken off once per sum.
+// (The conversion to 64-bit integers runs at a small fraction of the rate of these
+// adds: with it the 64-sequence case took 37 us.)
+constexpr uint32_t kHi = 0x41000000u, kLo = 0x37000000u;  // 8.0f, 2^-17
+__device__ __forceinline__ void weigh(float x, uint32_t& hi, uint32_t& lo) {
+    const float w = fminf(fmaxf(x, 0.f), 1.f);
+    const float h = __fadd_rz(w, 8.f);
+    hi = __float_as_uint(h);
+    lo = __float_as_uint(__fadd_rz(w - (h - 8.f), 7.62939453125e-6f));
+}
+// The sum of n weights from the sums of their parts (modulo 2^32: parts are below 2^20 + 1, n is at most 4).
+__device__ __forceinline__ uint64_t join(uint32_t hi, uint32_t lo, uint32_t n) {
+    return (static_cast<uint64_t>(hi - n * kHi) << 20) + (lo - n * kLo);
+}
+
+// p - q of entries i .. i + 3 (zero from `end` on), i a multiple of four; VEC: both
 // rows may be read 16 bytes at a time.
 template <bool VEC>
-__device__ __forceinline__ void four(const Weights& w, int64_t i, int64_t end, uint64_t (&out)[4]) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void four(const Weights& w, int i, int end, float (&x)[4]) {
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    x[0] = x[1] = x[2] = x[3] = 0.f;
     if (VEC && i + 4 <= end) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(w.p + i));
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
@@ -99,57 +107,66 @@ __device__ __forceinline__ void four(const Weights& w, int64_t i, int64_t end, u
                 if (w.q) y[e] = __ldg(w.q + i + e);
             }
     }
+    if (w.q) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = w.of(x[e], y[e], i + e);
+        for (int e = 0; e < 4; ++e) x[e] -= y[e];
+    } else if (static_cast<unsigned>(w.skip - i) < 4u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (w.skip == i + e) x[e] = 0.f;
+    }
 }
 
-// This lane's share of the weights of [lo, hi), and what it had added up before each
-// quarter of the run's steps (128 entries a step): the search starts at a quarter.
+__device__ __forceinline__ uint64_t sum4(const float (&x)[4]) {
+    uint32_t h = 0, l = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t hi, lo;
+        weigh(x[e], hi, lo);
+        h += hi;
+        l += lo;
+    }
+    return join(h, l, 4);
+}
+
+// This lane's share of the weights of [lo, hi), and what it had added up before the
+// second half of the run's steps (128 entries a step): the search starts at a half.
 template <bool VEC>
-__device__ __forceinline__ uint64_t run_sum(const Weights& w, int64_t lo, int64_t hi, int quarter, uint64_t (&marks)[3]) {
-    const int lane = threadIdx.x & 31, steps = static_cast<int>(cdiv<int64_t>(hi - lo, 128));
+__device__ __forceinline__ uint64_t run_sum(const Weights& w, int lo, int hi, int half, uint64_t& mark) {
+    const int lane = threadIdx.x & 31, steps = cdiv(hi - lo, 128);
     uint64_t sum = 0;
-    marks[0] = marks[1] = marks[2] = 0;
+    mark = 0;
 #pragma unroll 4
     for (int s = 0; s < steps; ++s) {
-        uint64_t e[4];
-        four<VEC>(w, lo + s * 128 + lane * 4, hi, e);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (s == (k + 1) * quarter) marks[k] = sum;
-        sum += (e[0] + e[1]) + (e[2] + e[3]);
+        float x[4];
+        four<VEC>(w, lo + s * 128 + lane * 4, hi, x);
+        if (s == half) mark = sum;
+        sum += sum4(x);
     }
-    // quarters that begin past the last step begin with everything
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-        if ((k + 1) * quarter >= steps) marks[k] = sum;
+    if (half >= steps) mark = sum;
     return sum;
 }
 
 // The smallest entry of [lo, hi) whose inclusive sum from lo exceeds `goal` (there is
-// one: the run's total does), given the marks of run_sum.
+// one: the run's total does), given the mark of run_sum.
 template <bool VEC>
-__device__ __forceinline__ int64_t run_search(const Weights& w, int64_t lo, int64_t hi, int quarter, uint64_t goal,
-                                              const uint64_t (&marks)[3]) {
+__device__ __forceinline__ int run_search(const Weights& w, int lo, int hi, int half, uint64_t goal, uint64_t mark) {
     const int lane = threadIdx.x & 31;
-    uint64_t skip = 0;
-    int64_t at = lo;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const uint64_t m = warp_sum64(marks[k]);
-        if (m <= goal) {
-            skip = m;
-            at = lo + static_cast<int64_t>(k + 1) * quarter * 128;
-        }
+    int at = lo;
+    mark = warp_sum64(mark);
+    if (mark <= goal) {
+        goal -= mark;
+        at = lo + half * 128;
     }
-    goal -= skip;
     constexpr int kAtOnce = 4;  // steps read together
     for (; at < hi; at += kAtOnce * 128) {
-        uint64_t e[kAtOnce][4], mine[kAtOnce], all = 0;
+        float x[kAtOnce][4];
+        uint64_t mine[kAtOnce], all = 0;
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s) four<VEC>(w, at + s * 128 + lane * 4, hi, x[s]);
 #pragma unroll
         for (int s = 0; s < kAtOnce; ++s) {
-            four<VEC>(w, at + s * 128 + lane * 4, hi, e[s]);
-            mine[s] = (e[s][0] + e[s][1]) + (e[s][2] + e[s][3]);
+            mine[s] = sum4(x[s]);
             all += mine[s];
         }
         all = warp_sum64(all);
@@ -170,9 +187,11 @@ __device__ __forceinline__ int64_t run_search(const Weights& w, int64_t lo, int6
                 int k = 0;
                 uint64_t sum = incl - mine[s];
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    sum += e[s][x];
-                    if (sum <= goal && k == x) ++k;
+                for (int e = 0; e < 3; ++e) {
+                    uint32_t h, l;
+                    weigh(x[s][e], h, l);
+                    sum += join(h, l, 1);
+                    if (sum <= goal && k == e) ++k;
                 }
                 const int src = __ffs(past) - 1;
                 return at + s * 128 + src * 4 + __shfl_sync(0xffffffffu, k, src);
@@ -228,16 +247,15 @@ __global__ void __launch_bounds__(kDraftThreads, 4) draft_verify_kernel(const Dr
         else
             w.skip = __ldg(x + count);
     }
-    const int64_t warps = int64_t(ctas) * kDraftWarps, mine = int64_t(rank) * kDraftWarps + warp;
-    const int64_t run = cdiv<int64_t>(cdiv<int64_t>(a.vocab, warps), 128) * 128;
-    const int64_t lo = min(mine * run, a.vocab), hi = min(lo + run, a.vocab);
-    const int quarter = static_cast<int>(cdiv<int64_t>(run / 128, 4));
-    uint64_t marks[3], part[kMaxCluster * kDraftWarps / 32], total = 0;
+    const int warps = static_cast<int>(ctas) * kDraftWarps, mine = static_cast<int>(rank) * kDraftWarps + warp;
+    const int vocab = static_cast<int>(a.vocab), run = cdiv(cdiv(vocab, warps), 128) * 128, half = cdiv(run / 128, 2);
+    const int lo = min(mine * run, vocab), hi = min(lo + run, vocab);
+    uint64_t mark, part[kMaxCluster * kDraftWarps / 32], total = 0;
     // Where the weights that a fallen draft leaves are all zero (p <= q
     // everywhere), the second pass draws from p itself.
     int pass = 0;
     for (;; ++pass) {
-        const uint64_t sum = warp_sum64(run_sum<VEC>(w, lo, hi, quarter, marks));
+        const uint64_t sum = warp_sum64(run_sum<VEC>(w, lo, hi, half, mark));
         if (lane == 0) totals[pass][warp] = sum;
         cluster_arrive();
         cluster_wait();
@@ -267,13 +285,13 @@ __global__ void __launch_bounds__(kDraftThreads, 4) draft_verify_kernel(const Dr
     uint64_t own = 0;
 #pragma unroll
     for (int k = 0; k < kMaxCluster * kDraftWarps / 32; ++k) {
-        const uint64_t v = __shfl_sync(0xffffffffu, part[k], static_cast<int>(mine & 31));
-        if (k == static_cast<int>(mine >> 5)) own = v;
+        const uint64_t v = __shfl_sync(0xffffffffu, part[k], mine & 31);
+        if (k == (mine >> 5)) own = v;
     }
     int* out = a.tokens + b * (a.drafts + 1);
     if (before <= goal && goal < before + own) {
-        const int64_t token = run_search<VEC>(w, lo, hi, quarter, goal - before, marks);
-        if (lane == 0) out[count] = static_cast<int>(token);
+        const int token = run_search<VEC>(w, lo, hi, half, goal - before, mark);
+        if (lane == 0) out[count] = token;
     }
     if (rank == 0 && warp == 0) {
         for (int i = lane; i <= a.drafts; i += 32)

@@ -89,7 +89,7 @@ __device__ __forceinline__ int sequence_of(const KvStep& s, int t) {
 // inv * (f C + e D), where the norm's weights are folded into the angles (A = w_e cos,
 // B = w_f sin, C = w_f cos, D = w_e sin) and inv is the head's reciprocal norm.
 struct Turn {
-    float A[4], B[4], C[4], D[4];
+    float2 A[2], B[2], C[2], D[2];
 };
 
 // Heads h, h + kPer, .. below `end` of one token, G lanes each: normed, rotated and
@@ -116,35 +116,40 @@ __device__ __forceinline__ void turn_heads(const TI* src, int64_t src_step, TO* 
                 e = {{u.x[0], u.x[2], w.x[0], w.x[2]}};
                 f = {{u.x[1], u.x[3], w.x[1], w.x[3]}};
             }
+            // pairs of elements at a time (packed fp32 instructions)
+            const float2 e2[2] = {make_float2(e.x[0], e.x[1]), make_float2(e.x[2], e.x[3])};
+            const float2 f2[2] = {make_float2(f.x[0], f.x[1]), make_float2(f.x[2], f.x[3])};
             float inv = 1.f;
             if (norm) {
-                float ss = 0.f;
+                float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ss = fmaf(e.x[i], e.x[i], fmaf(f.x[i], f.x[i], ss));
+                for (int i = 0; i < 2; ++i) ss = ffma2(e2[i], e2[i], ffma2(f2[i], f2[i], ss));
+                float sum = ss.x + ss.y;
 #pragma unroll
-                for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                inv = rsqrtf(fmaf(ss, inv_dim, eps));
+                for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                inv = rsqrtf(fmaf(sum, inv_dim, eps));
             }
+            const float2 zero = make_float2(0.f, 0.f), inv2 = make_float2(inv, inv);
             Run4 u, w;
-            if (turns) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u.x[i] = fmaf(e.x[i], c.A[i], -f.x[i] * c.B[i]);
-                    w.x[i] = fmaf(f.x[i], c.C[i], e.x[i] * c.D[i]);
+            for (int i = 0; i < 2; ++i) {
+                float2 x2, y2;
+                if (turns) {
+                    x2 = ffma2(f2[i], c.B[i], zero);
+                    x2 = ffma2(e2[i], c.A[i], make_float2(-x2.x, -x2.y));
+                    y2 = ffma2(f2[i], c.C[i], ffma2(e2[i], c.D[i], zero));
+                } else {  // past the rotated part: A and C alone
+                    x2 = ffma2(e2[i], c.A[i], zero);
+                    y2 = ffma2(f2[i], c.C[i], zero);
                 }
-            } else {  // past the rotated part: A and C alone
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u.x[i] = e.x[i] * c.A[i];
-                    w.x[i] = f.x[i] * c.C[i];
+                if (norm) {
+                    x2 = ffma2(x2, inv2, zero);
+                    y2 = ffma2(y2, inv2, zero);
                 }
-            }
-            if (norm) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u.x[i] *= inv;
-                    w.x[i] *= inv;
-                }
+                u.x[2 * i] = x2.x;
+                u.x[2 * i + 1] = x2.y;
+                w.x[2 * i] = y2.x;
+                w.x[2 * i + 1] = y2.y;
             }
             if (INTER) {
                 e = u;
@@ -217,11 +222,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const KvAp
         }
         Turn c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c.A[i] = wu.x[i] * cs.x[i];
-            c.B[i] = ww.x[i] * sn.x[i];
-            c.C[i] = ww.x[i] * cs.x[i];
-            c.D[i] = wu.x[i] * sn.x[i];
+        for (int i = 0; i < 2; ++i) {
+            const int j = 2 * i, k = j + 1;
+            c.A[i] = make_float2(wu.x[j] * cs.x[j], wu.x[k] * cs.x[k]);
+            c.B[i] = make_float2(ww.x[j] * sn.x[j], ww.x[k] * sn.x[k]);
+            c.C[i] = make_float2(ww.x[j] * cs.x[j], ww.x[k] * cs.x[k]);
+            c.D[i] = make_float2(wu.x[j] * sn.x[j], wu.x[k] * sn.x[k]);
         }
         return c;
     };

@@ -186,6 +186,20 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
 // Barrier of the compute warps (barrier 0 is __syncthreads).
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// Waits of a compute warp and its arrivals, without a branch that only one lane
+// takes: every lane tries the barrier; the bounded wait follows where that fails.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return warp_wait(bar, parity);
+}
+__device__ __forceinline__ void tile_free(uint64_t* bar, int lane) {
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                     smem_u32(bar)),
+                 "r"(lane)
+                 : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row r in a tile of `rows` rows whose
 // columns are stored as 64-column (128-byte) swizzled panels.
 __device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
@@ -641,7 +655,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     s[t][g][x] = 0.f;
                     if constexpr (QF32 || kTwo) s2[t][g][x] = 0.f;
                 }
-        if (ok) ok = warp_wait(&sm.k_full[kring.slot], kring.parity);
+        if (ok) ok = tile_wait(&sm.k_full[kring.slot], kring.parity);
         if (active) {
             const uint32_t kt = smem_u32(sm.k + kring.slot * P::kSlotBytes) + k_lane;
 #pragma unroll
@@ -693,8 +707,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                         for (int x = 0; x < 4; ++x) s[t][g][x] += s2[t][g][x];
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_empty[kring.slot]);
+        tile_free(&sm.k_empty[kring.slot], lane);
         kring.next();
         // ---- mask, running maximum and sum.  s[t][g][x]: token 16 t + quad + 8 (x / 2), row 2 qc + x % 2
         if (edge) {
@@ -749,7 +762,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
 #pragma unroll
             for (int x = 0; x < 2; ++x) l[g][x] = fmaf(l[g][x], f[g][x], sum[x]);
         }
-        if (ok) ok = warp_wait(&sm.v_full[vring.slot], vring.parity);
+        if (ok) ok = tile_wait(&sm.v_full[vring.slot], vring.parity);
         uint8_t* vtile = sm.v + vring.slot * P::kSlotBytes;
         if (edge) {
             // What no row sees (past the sequence's end, before every window) counts as
@@ -846,8 +859,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
             }
         }
         if (edge) fence_proxy_async_smem();  // cleared values, before the slot's next copy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_empty[vring.slot]);
+        tile_free(&sm.v_empty[vring.slot], lane);
         vring.next();
     }
 
