@@ -447,43 +447,52 @@ def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e
     return d
 
 
-def _token_rows(t, name, tokens, heads, dim):
-    """Pointer and token stride of [tokens, heads, head_dim] rows (heads adjacent within a token)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], not {list(t.shape)}")
-    n, h, d = t.shape
-    token, head, one = t.stride()
-    if n != tokens or h != heads or d != dim:
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], not {list(t.shape)}")
-    if one != 1 or (head != dim and h > 1):
+def _token_rows(t, name, shape):
+    """Pointer and token stride of rows [tokens, heads, head_dim] (heads adjacent within a token)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be adjacent")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr(), (token if tokens > 1 else h * dim)  # the stride of one token is never used
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1] * shape[2])  # one token's stride is never used
+
+
+def _stream_of(t, stream):
+    """The raw handle of `stream`, or of the current stream of the CUDA tensor t's device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True):
     """Stores a step's k and v [tokens, kv_heads, head_dim] in the cache and writes q [tokens, q_heads, head_dim] to
     q_out (may be q; both None: no queries), q and k normed and rotated as `rope` says.  Rows may be strided parts
     of one projection's output."""
-    n, dim = step.tokens, cache.head_dim
-    kp, ks = _token_rows(k, "k", n, cache.kv_heads, dim)
-    vp, vs = _token_rows(v, "v", n, cache.kv_heads, dim)
+    n, dim, dtype = step.tokens, cache.head_dim, k.dtype
+    shape = (n, cache.kv_heads, dim)
+    kp, ks = _token_rows(k, "k", shape)
+    vp, vs = _token_rows(v, "v", shape)
     qp = op = None
     qs = os_ = heads = 0
     if q is not None:
-        heads = q.shape[1]
-        qp, qs = _token_rows(q, "q", n, heads, dim)
+        shape = q.shape
+        heads = shape[1]
+        qp, qs = _token_rows(q, "q", (n, heads, dim))
         if q_out is not None:
-            op, os_ = _token_rows(q_out, "q_out", n, heads, dim)
-            if q_out.dtype != q.dtype:
+            op, os_ = _token_rows(q_out, "q_out", shape)
+            if q_out.dtype != dtype:
                 raise TypeError("q_out must have q's dtype")
+        if q.dtype != dtype:
+            raise TypeError("q, k and v must have one dtype")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    if v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    st = load_library().kv_append(cache.ref, step.ref, None if rope is None else rope.ref, qp, qs, heads, kp,
-                                  ks, vp, vs, _dtype_code(k), op, os_, _stream(stream))
+    st = load_library().kv_append(cache.ref, step.ref, None if rope is None else rope.ref, qp, qs, heads, kp, ks, vp, vs,
+                                  _dtype_code(k), op, os_, _stream_of(k, stream))
     if check:
         _check(st, "kv_append")
     return st
@@ -499,9 +508,10 @@ def kv_attention_workspace_size(q_heads, kv_heads, head_dim, max_new=1) -> int:
 def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, lse=None, stream=None, check=True):
     """Attention of the step's new tokens q [tokens, q_heads, head_dim] over the cache into out (same shape and
     dtype); scale defaults to head_dim ** -0.5, lse (f32 [tokens, q_heads]) is optional."""
-    n, dim, heads = step.tokens, cache.head_dim, q.shape[1]
-    qp, qs = _token_rows(q, "q", n, heads, dim)
-    op, os_ = _token_rows(out, "out", n, heads, dim)
+    n, dim, shape = step.tokens, cache.head_dim, q.shape
+    heads = shape[1]
+    qp, qs = _token_rows(q, "q", (n, heads, dim))
+    op, os_ = _token_rows(out, "out", shape)
     if out.dtype != q.dtype:
         raise TypeError("out must have q's dtype")
     lp = None
@@ -516,7 +526,7 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
                                 dtype=torch.uint8, device=q.device)
     st = load_library().kv_attention(cache.ref, step.ref, qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
-                                     _packed(workspace, "workspace", None), workspace.nbytes, _stream(stream))
+                                     _packed(workspace, "workspace", None), workspace.nbytes, _stream_of(q, stream))
     if check:
         _check(st, "kv_attention")
     return st
@@ -533,24 +543,24 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
         raise ValueError("draft must be [batch, n, vocab]")
     if n == 0:
         draft = None  # nothing was drafted
-    for t, name in ((target, "target"), (draft, "draft")):
-        if t is not None and vocab > 1 and t.stride(2) != 1:
+    def rows_of(t, name, count):  # pointer and strides (those of an extent of one are never used)
+        s0, s1, s2 = t.stride()
+        if s2 != 1 and vocab > 1:
             raise ValueError(f"{name} must have unit stride along the vocabulary")
-    for t, shape, name in ((draft_tokens, (batch, n), "draft_tokens"), (uniforms, (batch, rows), "uniforms"),
-                           (tokens, (batch, rows), "tokens"), (accepted, (batch,), "accepted"),
-                           (n_drafts, (batch,), "n_drafts")):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
+        return _on_gpu(t, name, f32), (s0 if batch > 1 else count * vocab), (s1 if count > 1 else vocab)
 
-    def strides(t, n):  # those of an extent of one are never used
-        return (t.stride(0) if batch > 1 else n * vocab), (t.stride(1) if n > 1 else vocab)
-    ts, tr = strides(target, rows)
-    ds, dr = (0, 0) if draft is None else strides(draft, n)
-    st = load_library().draft_verify(_on_gpu(target, "target", f32), ts, tr, _on_gpu(draft, "draft", f32), ds, dr,
-                                     _packed(draft_tokens, "draft_tokens", i32), _packed(n_drafts, "n_drafts", i32),
-                                     _packed(uniforms, "uniforms", f32), batch, n, vocab,
-                                     _packed(tokens, "tokens", i32), _packed(accepted, "accepted", i32),
-                                     _stream(stream))
+    def whole(t, name, shape, dtype):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+        return _packed(t, name, dtype)
+
+    tp, ts, tr = rows_of(target, "target", rows)
+    dp, ds, dr = (None, 0, 0) if draft is None else rows_of(draft, "draft", n)
+    st = load_library().draft_verify(tp, ts, tr, dp, ds, dr, whole(draft_tokens, "draft_tokens", (batch, n), i32),
+                                     None if n_drafts is None else whole(n_drafts, "n_drafts", (batch,), i32),
+                                     whole(uniforms, "uniforms", (batch, rows), f32), batch, n, vocab,
+                                     whole(tokens, "tokens", (batch, rows), i32), whole(accepted, "accepted", (batch,), i32),
+                                     _stream_of(target, stream))
     if check:
         _check(st, "draft_verify")
     return st
