@@ -214,6 +214,8 @@ __global__ void __launch_bounds__(kDraftThreads, 4) draft_verify_kernel(const Dr
     const float* u = a.uniforms + b * (a.drafts + 1);
     const float* target = a.target + b * a.target_seq;
     const float* draft = a.draft ? a.draft + b * a.draft_seq : nullptr;
+    int tok = lane < a.drafts ? __ldg(x + lane) : -1;
+    float chance = lane < a.drafts ? __ldg(u + lane) : 0.f;
     const int given = a.n_drafts ? min(max(__ldg(a.n_drafts + b), 0), a.drafts) : a.drafts;
 
     // ---- how many drafts stand
@@ -221,14 +223,15 @@ __global__ void __launch_bounds__(kDraftThreads, 4) draft_verify_kernel(const Dr
     int count = 0;
     for (int i0 = 0; i0 < given; i0 += 32) {
         const int i = i0 + lane;
+        if (i0 > 0) {  // (the first 32 were asked for together with their number)
+            tok = i < given ? __ldg(x + i) : -1;
+            chance = i < given ? __ldg(u + i) : 0.f;
+        }
         bool ok = false;
-        if (i < given) {
-            const int64_t tok = __ldg(x + i);
-            if (tok >= 0 && tok < a.vocab) {
-                const float p = __ldg(target + i * a.target_row + tok);
-                const float q = draft ? __ldg(draft + i * a.draft_row + tok) : 1.f;
-                ok = __fmul_rn(__ldg(u + i), q) < p;
-            }
+        if (i < given && tok >= 0 && tok < a.vocab) {
+            const float p = __ldg(target + i * a.target_row + tok);
+            const float q = draft ? __ldg(draft + i * a.draft_row + tok) : 1.f;
+            ok = __fmul_rn(chance, q) < p;
         }
         const unsigned fell = ~__ballot_sync(0xffffffffu, ok);
         count = i0 + (fell ? __ffs(fell) - 1 : 32);

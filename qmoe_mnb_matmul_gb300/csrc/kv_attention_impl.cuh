@@ -640,6 +640,9 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     for (int i = 0; i < nt; ++i, tok0 += kKvTile) {
         // tokens that not every row sees
         const bool edge = tok0 < w.t.lo_all || tok0 + TOK > w.t.hi_all;
+        // none of them is seen by any row: the warp only keeps the rings' order (with
+        // more rows the registers that this takes cost more than it saves)
+        const bool none = ROWS == 8 && (tok0 >= w.t.hi || tok0 + TOK <= w.t.lo);
         // ---- scores.  With fp32 queries each product of the leading part starts from
         // zero, is added outside, and the smaller parts are added last; otherwise two
         // accumulators take turns along the head dimension where a warp has no other
@@ -656,7 +659,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     if constexpr (QF32 || kTwo) s2[t][g][x] = 0.f;
                 }
         if (ok) ok = tile_wait(&sm.k_full[kring.slot], kring.parity);
-        if (active) {
+        if (active && !none) {
             const uint32_t kt = smem_u32(sm.k + kring.slot * P::kSlotBytes) + k_lane;
 #pragma unroll
             for (int kp = 0; kp < KS / 2; ++kp) {  // two steps along the head dimension
@@ -709,6 +712,12 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
         }
         tile_free(&sm.k_empty[kring.slot], lane);
         kring.next();
+        if (none) {
+            if (ok) ok = tile_wait(&sm.v_full[vring.slot], vring.parity);
+            tile_free(&sm.v_empty[vring.slot], lane);
+            vring.next();
+            continue;
+        }
         // ---- mask, running maximum and sum.  s[t][g][x]: token 16 t + quad + 8 (x / 2), row 2 qc + x % 2
         if (edge) {
 #pragma unroll
@@ -770,11 +779,13 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
             // infinity or a NaN that some rows see must not reach the others as 0 * inf:
             // it is cleared too once each row that sees it has added it (its weight, a
             // positive number, changes nothing).
+            // (Tokens that every row sees, [first, last) of the warp's, need neither.)
+            const int first = min(max(w.t.lo_all - tok0, 0), TOK), last = min(max(w.t.hi_all - tok0, first), TOK);
             auto scan = [&](bool clear_odd) {
                 bool odd = false;
 #pragma unroll 1
-                for (int x = wr * 32 + lane; x < TOK * (DP / 8); x += 32 * WR) {
-                    const int e = x / (DP / 8), j = tok0 + e;
+                for (int x = wr * 32 + lane; x < (TOK - (last - first)) * (DP / 8); x += 32 * WR) {
+                    const int e = x / (DP / 8) < first ? x / (DP / 8) : x / (DP / 8) + last - first, j = tok0 + e;
                     uint4* at = reinterpret_cast<uint4*>(vtile + tile_at(kKvTile, wt * TOK + e, x % (DP / 8)));
                     uint4 v = *at;
                     const bool out = j < w.t.lo || j >= w.t.hi;
