@@ -433,7 +433,8 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * kv_heads).  A row that sees nothing gives zeros.  lse [tokens, q_heads] (or
  * NULL) gets m + ln(sum), -infinity for such a row.
  * q, out [tokens, q_heads, head_dim] in dtype (f32 or the cache's) with strides
- * in elements between tokens, whole 16-byte units.  scale > 0 and finite.
+ * in elements between tokens, whole 16-byte units; out may be q itself.  scale >
+ * 0 and finite.
  * Scores, statistics and sums are fp32; the probabilities carry at least 16
  * significant bits (fp32 output: 22) into the product with the values.  The
  * results do not depend on which other sequences share the step in more than

@@ -524,6 +524,8 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
         import torch
         workspace = torch.empty(kv_attention_workspace_size(heads, cache.kv_heads, dim, step.max_new),
                                 dtype=torch.uint8, device=q.device)
+        if stream is not None:  # the allocation belongs to the current stream and is given back at return
+            workspace.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
     st = load_library().kv_attention(cache.ref, step.ref, qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
                                      _packed(workspace, "workspace", None), workspace.nbytes, _stream_of(q, stream))

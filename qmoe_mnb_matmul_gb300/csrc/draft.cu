@@ -110,7 +110,7 @@ __device__ __forceinline__ void four(const Weights& w, int i, int end, float (&x
     if (w.q) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] -= y[e];
-    } else if (static_cast<unsigned>(w.skip - i) < 4u) {
+    } else if (static_cast<unsigned>(w.skip) - static_cast<unsigned>(i) < 4u) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (w.skip == i + e) x[e] = 0.f;

@@ -60,6 +60,7 @@ mnb_status check_step(const kv_step_desc* d, const KvCache& c, KvStep* s, bool* 
     }
     if (!d->seq_lens || !d->page_table || d->max_pages < 1 || d->table_stride < d->max_pages) return MNB_ERR_INVALID_ARG;
     if (!d->new_start && d->tokens != d->batch) return MNB_ERR_INVALID_ARG;
+    if (d->tokens > (1 << 30)) return MNB_ERR_SIZE_OVERFLOW;  // token and row numbers are 32-bit
     if (!aligned(d->seq_lens, 4) || !aligned(d->new_start, 4) || !aligned(d->page_table, 4)) return MNB_ERR_UNSUPPORTED;
     int64_t total = 0;
     if (!span_ok(d->batch, d->table_stride, &total)) return MNB_ERR_SIZE_OVERFLOW;
@@ -170,7 +171,7 @@ mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, co
     if (dtype != MNB_F32 && dtype != a.cache.dtype) return MNB_ERR_UNSUPPORTED;
     if (nothing) return MNB_OK;
     if (!q || !out) return MNB_ERR_INVALID_ARG;
-    if (q_heads > kMaxInt / (a.cache.dim * 4) || step->tokens > kMaxInt / q_heads) return MNB_ERR_SIZE_OVERFLOW;
+    if (q_heads > kMaxInt / (a.cache.dim * 4) || step->tokens > (int64_t(1) << 30) / q_heads) return MNB_ERR_SIZE_OVERFLOW;
     if ((st = check_rows(q, q_stride, q_heads, a.cache.dim, a.step.tokens)) != MNB_OK) return st;
     if ((st = check_rows(out, out_stride, q_heads, a.cache.dim, a.step.tokens)) != MNB_OK) return st;
     if (!aligned(lse, 4)) return MNB_ERR_UNSUPPORTED;

@@ -225,6 +225,11 @@ struct Walk {
     RowTile t;
 };
 
+// The first token that the row at position pos sees (window 0: every earlier one).
+__device__ __forceinline__ int window_start(int window, int pos) {
+    return window > 0 && pos >= window ? pos + 1 - window : 0;
+}
+
 template <int ROWS>
 __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int pos0, int rt) {
     RowTile t;
@@ -235,8 +240,8 @@ __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int 
     const int cap = a.step.capacity;
     t.hi = min(max(pos0 + tok1 + 1, 0), cap);
     t.hi_all = min(max(pos0 + tok0 + 1, 0), cap);
-    t.lo = a.window > 0 ? max(0, pos0 + tok0 + 1 - a.window) : 0;
-    t.lo_all = a.window > 0 ? max(0, pos0 + tok1 + 1 - a.window) : 0;
+    t.lo = window_start(a.window, pos0 + tok0);
+    t.lo_all = window_start(a.window, pos0 + tok1);
     // a tile of more than 32 rows takes about twice the time of one that HBM bounds
     // (its matrix instructions bound it: measured 4900 against 2700 cycles)
     t.cost = ROWS > 32 && t.rows > 32 ? 2 : 1;
@@ -633,7 +638,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     auto sees = [&](int rr, int& lo, int& hi) {
         const int pos = w.pos0 + a.by_group(w.t.first_row + rr);
         hi = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
-        lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+        lo = window_start(a.window, pos);
     };
 
 #pragma unroll 1

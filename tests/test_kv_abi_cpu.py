@@ -53,7 +53,7 @@ BAD_CACHE = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(num_pages=0
 BAD_STEP = [(dict(seq_lens=None), INVALID), (dict(page_table=None), INVALID), (dict(batch=-1), INVALID),
             (dict(tokens=-1), INVALID), (dict(max_new=0), INVALID), (dict(max_pages=0), INVALID),
             (dict(table_stride=9), INVALID), (dict(new_start=None), INVALID),  # 9 tokens of 4 sequences
-            (dict(seq_lens=FAKE + 2), UNSUPPORTED), (dict(table_stride=1 << 61), OVERFLOW)]
+            (dict(tokens=(1 << 30) + 1), OVERFLOW), (dict(seq_lens=FAKE + 2), UNSUPPORTED), (dict(table_stride=1 << 61), OVERFLOW)]
 
 
 @pytest.mark.parametrize("bad,code", BAD_CACHE)
@@ -117,6 +117,7 @@ def test_attention_errors(lib):
     assert attention(lib, size=1000) == WORKSPACE
     assert attention(lib, ws=FAKE + 128) == UNSUPPORTED
     assert attention(lib, qh=1 << 40, qs=1 << 50) == OVERFLOW
+    assert attention(lib, s=step(tokens=(1 << 26) + 1)) == OVERFLOW   # 16 heads: 2^30 rows
 
 
 def test_attention_workspace(lib):

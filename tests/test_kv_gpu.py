@@ -267,6 +267,36 @@ def test_unseen_tokens_never_reach_a_row():
                 assert bool(torch.isfinite(seen[:, 1::3]).all())
 
 
+def test_a_bad_query_spoils_its_own_row_only():
+    g = rng("badquery")
+    bt = Batch(g, [130, 64], [3, 1], 2, 128, 16, "bf16")
+    bt.fill(g)
+    for dtype in ("bf16", "f32"):
+        q = torch.randn((4, 8, 128), generator=g, device="cuda").to(DT[dtype])
+        clean = torch.empty_like(q)
+        mnb.kv_attention(bt.cache, bt.step, q, clean)
+        out = torch.empty_like(q)
+        for bad in (math.nan, math.inf):
+            spoiled = q.clone()
+            spoiled[1, 2, 5] = bad
+            mnb.kv_attention(bt.cache, bt.step, spoiled, out)
+            rows = torch.ones((4, 8), dtype=torch.bool, device="cuda")
+            rows[1, 2] = False
+            assert torch.equal(out[rows], clean[rows])
+            assert not bool(torch.isfinite(out[1, 2]).any())
+
+
+@pytest.mark.parametrize("lens", [[40], [9000, 70]])  # within one CTA's range, split over many
+def test_output_in_place_of_the_queries(lens):
+    g = rng("alias", tuple(lens))
+    bt = Batch(g, lens, [2] * len(lens), 2, 128, 16, "bf16")
+    bt.fill(g)
+    q, out, _ = attend(bt, g, 3, "bf16")
+    same = q.clone()
+    mnb.kv_attention(bt.cache, bt.step, same, same)
+    assert torch.equal(same, out)
+
+
 def test_window_leaves_bad_old_tokens_behind():
     g = rng("old")
     bt = Batch(g, [200], [4], 1, 64, 16, "f16")
@@ -370,6 +400,12 @@ def test_another_stream_and_a_captured_graph():
     mnb.kv_attention(bt.cache, bt.step, q, other, ws, stream=s)
     s.synchronize()
     assert torch.equal(out, other)
+    for handle in (s, s.cuda_stream):  # without a workspace the call makes one for that stream
+        other.zero_()
+        s.wait_stream(torch.cuda.current_stream())
+        mnb.kv_attention(bt.cache, bt.step, q, other, stream=handle)
+        s.synchronize()
+        assert torch.equal(out, other)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         mnb.kv_attention(bt.cache, bt.step, q, other, ws)
