@@ -23,11 +23,35 @@ MNB_SLICE_DECL(kv_attention_bf16_qf32)
 namespace {
 
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a split pair's parts in
-// range order.  One CTA per (CTA of the main kernel that begins a split pair, row
-// of the pair); its warps share the parts.  The parts come from L2 (2.5 MB in all
-// with 8-row tiles); what it costs is the launch and two dependent loads (the
-// record, then a warp's first parts together with the statistics), so it is kept
-// small: eight rows at a time in 256 threads took 2.4 us longer.
+// range order.  CTAs blockIdx.x of the grid join the pair that begins in CTA
+// blockIdx.x of the main kernel: the four warps of a CTA share the parts of a row; of
+// more rows than CTAs, in up to kFewParts parts, each warp joins rows by itself (40
+// rows of drafts: 78 us in all instead of 85 with a CTA for each row; with one
+// sequence's two rows in 13 parts it is the slower way, 8.9 us instead of 7.2).
+// The parts come from L2 (2.5 MB in all with
+// 8-row tiles); what it costs is the launch and two dependent loads (the record,
+// then the first parts together with the statistics), so it is kept small: eight
+// rows at a time in 256 threads took 2.4 us longer.
+constexpr int kFewParts = 16;
+constexpr int kJoinGridY = 16;  // CTAs of a pair
+
+// Writes columns d, d + 1 of a row (lane's share of it) and the row's log-sum-exp.
+template <int DP>
+__device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, int flat, int head_kv, int d, float2 s,
+                                           float m, float l) {
+    const int tok = a.by_group(flat), head = head_kv * a.group + flat - tok * a.group;
+    const int64_t token = tok;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+    if (d < a.cache.dim) {
+        const int64_t at = token * a.out_stride + static_cast<int64_t>(head) * a.cache.dim + d;
+        store_from_f32(a.out, out_dtype, at, s.x * inv);
+        store_from_f32(a.out, out_dtype, at + 1, s.y * inv);
+    }
+    if (a.lse && d == 0)
+        a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int rows_per_tile, int out_dtype) {
     constexpr int NV = DP / 64;    // float2 per lane
@@ -41,6 +65,35 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
     const int4 j = a.join[c];
     if (j.x < 0) return;
     const int n = j.x - c + 1, rows = j.y >> 1, slot0 = 2 * c + (j.y & 1), head_kv = j.w;
+    if (rows > kJoinGridY && n <= kFewParts) {
+#pragma unroll 1
+        for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
+            auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * rows_per_tile + row; };
+            const float2 ml = lane < n ? a.part_ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+            float2 acc[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] = make_float2(0.f, 0.f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float w = lane < n ? exp2f(ml.x - (m == -INFINITY ? 0.f : m)) : 0.f;
+            const float l = warp_sum(w * ml.y);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float2* o = reinterpret_cast<const float2*>(a.part_o + slot(i) * DP) + lane;
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const float2 x = o[v * 32];
+                    acc[v].x = fmaf(wi, x.x, acc[v].x);
+                    acc[v].y = fmaf(wi, x.y, acc[v].y);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < NV; ++v) join_store<DP>(a, out_dtype, j.z + row, head_kv, (v * 32 + lane) * 2, acc[v], m, l);
+        }
+        return;
+    }
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
         auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * rows_per_tile + row; };
         auto o_at = [&](int i) { return reinterpret_cast<const float2*>(a.part_o + slot(i) * DP) + lane; };
@@ -104,26 +157,14 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
 #pragma unroll
         for (int v = 0; v < NV; ++v) sums[warp][v * 32 + lane] = acc[v];
         __syncthreads();
-        const int flat = j.z + row, tok = a.by_group(flat);
-        const int64_t token = tok;
-        const int head = head_kv * a.group + flat - tok * a.group;
         if (threadIdx.x < 32 * NV) {
-            const int d = threadIdx.x * 2;
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
             float2 s = sums[0][threadIdx.x];
 #pragma unroll
             for (int x = 1; x < 4; ++x) {
                 s.x += sums[x][threadIdx.x].x;
                 s.y += sums[x][threadIdx.x].y;
             }
-            if (d < a.cache.dim) {
-                const int64_t at = token * a.out_stride + static_cast<int64_t>(head) * a.cache.dim + d;
-                store_from_f32(a.out, out_dtype, at, s.x * inv);
-                store_from_f32(a.out, out_dtype, at + 1, s.y * inv);
-            }
-            if (a.lse && threadIdx.x == 0)
-                a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-                    l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            join_store<DP>(a, out_dtype, j.z + row, head_kv, threadIdx.x * 2, s, m, l);
         }
         __syncthreads();
     }
@@ -200,7 +241,8 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);
     int ctas = 0;
     if ((e = slice(kmap, vmap, a, rows, pad, sm_count, pdl, stream, &ctas)) != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min<int64_t>(rows, a.group * max_new)));
+    const dim3 grid(static_cast<unsigned>(ctas), 
+                    static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(rows, a.group * max_new), kJoinGridY)));
     if (pad == 64) return launch_ready<kv_join_kernel<64>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
     if (pad == 128) return launch_ready<kv_join_kernel<128>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
     return launch_ready<kv_join_kernel<256>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
