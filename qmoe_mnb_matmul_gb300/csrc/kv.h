@@ -91,7 +91,7 @@ struct KvAttnArgs {
     int64_t out_stride;
     float* lse;  // [tokens, q_heads] or null
     int group;   // query heads per key-value head
-    FastDiv by_group;
+    FastDiv by_group, by_page;  // division by group, by the page size
     float scale;
     int window;  // 0: every earlier token
     int box_rows;

@@ -230,6 +230,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     a.part_ml = reinterpret_cast<float2*>(ws + sp.part_ml);
     a.join = reinterpret_cast<int4*>(ws + sp.join);
     a.by_group.set(static_cast<uint32_t>(a.group));
+    a.by_page.set(static_cast<uint32_t>(a.cache.page_size));
     // a TMA box holds as many rows as divide a page (at least 8, at most a tile)
     a.box_rows = kKvTile;
     while (a.cache.page_size % a.box_rows) a.box_rows >>= 1;

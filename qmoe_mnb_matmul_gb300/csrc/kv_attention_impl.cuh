@@ -288,33 +288,40 @@ __device__ __forceinline__ void next_pair(const KvAttnArgs& a, Walk& w) {
     w.t = row_tile<ROWS>(a, w.count, w.pos0, w.rt);
 }
 
-// floor(total * c / ctas) for c <= ctas <= kKvMaxCtas, in 32 bits where that
-// holds the product (a 64-bit division costs as much as a load).
-__device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) {
-    if (total < (int64_t(1) << 32) / kKvMaxCtas)
-        return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
-    return total * c / ctas;
-}
-
-// The CTA's range of units.
+// The CTA's range of units.  CTA c of the `ctas` that have units takes `each` of them,
+// the first `more` CTAs one more.
 struct Range {
-    int64_t at, end, total;
-    int ctas;  // CTAs that have units
+    int64_t at, end, each;
+    int ctas, more;
+
+    __device__ __forceinline__ void divide(int64_t total) {  // (a 64-bit division costs as much as a load)
+        each = total < (int64_t(1) << 32) ? static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas) : total / ctas;
+        more = static_cast<int>(total - each * ctas);
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return each * c + min(c, more); }
+    // The CTA that unit u falls to.
+    __device__ __forceinline__ int owner(int64_t u) const {
+        const int64_t longer = (each + 1) * more;
+        if (u < longer) return static_cast<int>(u / (each + 1));
+        return more + static_cast<int>((u - longer) / each);
+    }
 };
 
 // The range and the walk's start, worked out by each warp for itself: the lanes
 // take 32 sequences at a time, once for the total and once (kept in registers
 // where 32 are all there are) to find the sequence that the range begins in.
 // The way from the launch to the first copy passes through here, so it is short
-// rather than general: one load of lengths, two 32-bit divisions.
+// rather than general: one load of lengths, two 32-bit divisions (one of the units,
+// one of the pair).
 template <int ROWS>
 __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     const int lane = threadIdx.x & 31, batch = a.step.batch;
     Walk mine = {};
     int64_t tiles = 0, incl = 0, before = 0;
     Range r;
-    r.total = r.at = r.end = 0;
-    r.ctas = 0;
+    int64_t total = 0;
+    r.at = r.end = r.each = 0;
+    r.ctas = r.more = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -334,7 +341,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
             }
             const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
             if (pass == 0) {
-                r.total += all;
+                total += all;
             } else {
                 // units here are those of one head: a sequence's heads come one after the other
                 const int64_t begin = before + (incl - tiles) * a.cache.heads, end = before + incl * a.cache.heads;
@@ -374,14 +381,15 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
             }
         }
         if (pass == 0) {
-            r.total *= a.cache.heads;
+            total *= a.cache.heads;
             // a range holds a tile's first unit: as many units as the dearest tile has
-            r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), r.total / (ROWS > 32 ? 2 : 1)));
+            r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total / (ROWS > 32 ? 2 : 1)));
+            if (total > 0 && r.ctas == 0) r.ctas = 1;
             const int c = blockIdx.x;
-            if (r.total > 0 && r.ctas == 0) r.ctas = 1;
             if (c >= r.ctas) return r;  // fewer units than CTAs
-            r.at = share(r.total, c, r.ctas);
-            r.end = share(r.total, c + 1, r.ctas);
+            r.divide(total);
+            r.at = r.start(c);
+            r.end = r.start(c + 1);
         }
     }
     r.end = r.at;  // not reached: the range begins in some sequence
@@ -452,7 +460,7 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
     const int lane = threadIdx.x & 31;
     const int R = a.box_rows, blocks = kKvTile / R, ps = a.cache.page_size;
     const int panel = lane / blocks, row0 = (lane % blocks) * R;
-    const int step_pages = kKvTile / ps, step_rows = kKvTile % ps;
+    const int step_pages = a.by_page(kKvTile), step_rows = kKvTile - step_pages * ps;
     const bool issues = panel < DP / 64;
     const uint32_t dst = smem_u32(slots) + panel * (kKvTile * 128) + row0 * 128;
     Ring<SLOTS> ring;
@@ -464,8 +472,9 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
         int tok = (w.t.lo / kKvTile + w.tile) * kKvTile + row0;
         // page and row of the box at token tok; boxes that no row sees are asked for
         // outside the cache, which fills them with zeros and reads nothing
-        const int* at_page = a.step.page_table + w.b * a.step.table_stride + tok / ps;
-        int row = tok % ps;
+        const int index = a.by_page(tok);
+        const int* at_page = a.step.page_table + w.b * a.step.table_stride + index;
+        int row = tok - index * ps;
         auto wanted = [&] { return issues && tok < w.t.hi && tok + R > w.t.lo; };
         int page = wanted() ? load_now(at_page) : -1;
         for (int i = 0; i < nt; ++i) {
@@ -1053,10 +1062,8 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
             }
         }
         if (w.tile == 0 && !whole) {  // the pair begins here and goes on in the next CTAs
-            // the CTA of the pair's last tile: the largest c whose range starts at or before its first unit
-            join = make_int4(static_cast<int>(((at + (w.t.tiles - 1) * w.t.cost + 1) * r.ctas - 1) / r.total),
-                             2 * w.t.rows + slot,
-                             w.first * a.group + w.t.first_row, w.h);
+            // (a tile belongs to the CTA that its first unit falls to)
+            join = make_int4(r.owner(at + static_cast<int64_t>(w.t.tiles - 1) * w.t.cost), 2 * w.t.rows + slot, w.first * a.group + w.t.first_row, w.h);
         }
         at += nt * w.t.cost;
         w.tile += nt;
