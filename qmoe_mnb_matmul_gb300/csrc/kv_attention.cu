@@ -242,7 +242,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);
     int ctas = 0;
     if ((e = slice(kmap, vmap, a, rows, pad, sm_count, pdl, stream, &ctas)) != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(ctas), 
+    const dim3 grid(static_cast<unsigned>(ctas),
                     static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(rows, a.group * max_new), kJoinGridY)));
     if (pad == 64) return launch_ready<kv_join_kernel<64>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);
     if (pad == 128) return launch_ready<kv_join_kernel<128>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);

@@ -42,6 +42,15 @@
 // tile start from zero and are added to the running fp32 sum outside, because
 // the tensor core's own accumulation truncates: over a long cache that would
 // drift.
+//
+// Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens,
+// 16 query heads over 8, 1.09 GB: 173 us, 6.3 TB/s; one sequence of 131072 tokens, 32
+// over 4, 268 MB: 50 us; 777 tokens: 7.1 us, all latency (finding the range 1.5, the
+// first tile 2.5, the join 2).  16 sequences with 1 .. 5 drafts, 24 .. 40 rows, 294 MB:
+// 79 us, bound by the latency of the matrix instructions (two compute warps per
+// scheduler, tensor pipe 33 % busy).  What was slower: rows on the instructions' long
+// side (187 us for the batch), one producer warp for keys and values (219), a page
+// lookup that a tile waits for (344).
 #pragma once
 
 #include <cuda.h>
