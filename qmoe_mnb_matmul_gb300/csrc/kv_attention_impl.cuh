@@ -316,96 +316,99 @@ struct Range {
     }
 };
 
-// The range and the walk's start, worked out by each warp for itself: the lanes
-// take 32 sequences at a time, once for the total and once (kept in registers
-// where 32 are all there are) to find the sequence that the range begins in.
-// The way from the launch to the first copy passes through here, so it is short
-// rather than general: one load of lengths, two 32-bit divisions (one of the units,
-// one of the pair).
-template <int ROWS>
-__device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
-    const int lane = threadIdx.x & 31, batch = a.step.batch;
-    Walk mine = {};
-    int64_t tiles = 0, incl = 0, before = 0;
-    Range r;
-    int64_t total = 0;
-    r.at = r.end = r.each = 0;
-    r.ctas = r.more = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-        for (int s0 = 0; s0 < batch; s0 += 32) {
-            if (pass == 0 || batch > 32) {
-                tiles = 0;
-                if (s0 + lane < batch) {
-                    load_sequence<ROWS>(a, mine, s0 + lane);
-                    tiles = sequence_units<ROWS>(a, mine);
-                }
-                incl = tiles;
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += v;
-                }
-            }
-            const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
-            if (pass == 0) {
-                total += all;
-            } else {
-                // units here are those of one head: a sequence's heads come one after the other
-                const int64_t begin = before + (incl - tiles) * a.cache.heads, end = before + incl * a.cache.heads;
-                const unsigned owner = __ballot_sync(0xffffffffu, begin <= r.at && r.at < end);
-                if (owner) {
-                    const int src = __ffs(owner) - 1;
-                    w.b = s0 + src;
-                    w.first = __shfl_sync(0xffffffffu, mine.first, src);
-                    w.count = __shfl_sync(0xffffffffu, mine.count, src);
-                    w.pos0 = __shfl_sync(0xffffffffu, mine.pos0, src);
-                    w.row_tiles = __shfl_sync(0xffffffffu, mine.row_tiles, src);
-                    int64_t off = r.at - __shfl_sync(0xffffffffu, begin, src);
-#pragma unroll 1
-                    for (w.rt = 0;; ++w.rt) {
-                        w.t = row_tile<ROWS>(a, w.count, w.pos0, w.rt);
-                        const int64_t n = static_cast<int64_t>(w.t.tiles) * w.t.cost * a.cache.heads;
-                        if (off < n) break;
-                        off -= n;
-                    }
-                    const int pair = w.t.tiles * w.t.cost;  // units of a pair: below 2^27
-                    if (off < (int64_t(1) << 31)) {
-                        w.h = static_cast<int>(off) / pair;
-                        w.tile = static_cast<int>(off) - w.h * pair;
-                    } else {
-                        w.h = static_cast<int>(off / pair);
-                        w.tile = static_cast<int>(off % pair);
-                    }
-                    if (ROWS > 32 && w.t.cost == 2) {
-                        // a tile belongs to the CTA that its first unit falls to
-                        r.at += w.tile & 1;
-                        w.tile = (w.tile + 1) >> 1;
-                        if (w.tile == w.t.tiles && r.at < r.end) next_pair<ROWS>(a, w);
-                    }
-                    return r;
-                }
-                before += all * a.cache.heads;
-            }
-        }
-        if (pass == 0) {
-            total *= a.cache.heads;
-            // a range holds a tile's first unit: as many units as the dearest tile has
-            r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total / (ROWS > 32 ? 2 : 1)));
-            if (total > 0 && r.ctas == 0) r.ctas = 1;
-            const int c = blockIdx.x;
-            if (c >= r.ctas) return r;  // fewer units than CTAs
-            r.divide(total);
-            r.at = r.start(c);
-            r.end = r.start(c + 1);
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (static_cast<int>(threadIdx.x & 31) >= o) v += x;
     }
-    r.end = r.at;  // not reached: the range begins in some sequence
-    return r;
+    return v;
 }
 
-// ------------------------------------------------------------- the kernel
+// The range and the walk's start, worked out by each warp for itself: a lane adds up
+// an equal share of consecutive sequences (their loads do not wait for one another),
+// and where that is more than one sequence, the warp looks through the share that
+// the range begins in again.  The way from the launch to the first copy passes
+// through here, so it is short rather than general: with up to 32 sequences one load
+// of lengths, two 32-bit divisions (one of the units, one of the pair).
+template <int ROWS>
+__device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
+    const int lane = threadIdx.x & 31, batch = a.step.batch, per = (batch + 31) / 32;
+    const int64_t heads = a.cache.heads;
+    Walk mine = {};
+    int64_t units = 0;
+#pragma unroll 4
+    for (int s = lane * per; s < min((lane + 1) * per, batch); ++s) {
+        load_sequence<ROWS>(a, mine, s);
+        units += sequence_units<ROWS>(a, mine);
+    }
+    units *= heads;
+    int64_t incl = warp_scan(units);
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    Range r;
+    r.at = r.end = r.each = 0;
+    r.more = 0;
+    // a range holds a tile's first unit: as many units as the dearest tile has
+    r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total / (ROWS > 32 ? 2 : 1)));
+    if (total > 0 && r.ctas == 0) r.ctas = 1;
+    const int c = blockIdx.x;
+    if (c >= r.ctas) return r;  // fewer units than CTAs
+    r.divide(total);
+    r.at = r.start(c);
+    r.end = r.start(c + 1);
+    int64_t begin = incl - units;  // of this lane's share
+    int src = __ffs(__ballot_sync(0xffffffffu, begin <= r.at && r.at < incl)) - 1;
+    w.b = src;
+    if (per > 1) {
+        const int last = min((src + 1) * per, batch);
+        int64_t before = __shfl_sync(0xffffffffu, begin, src);
+#pragma unroll 1
+        for (int s0 = src * per; s0 < last; s0 += 32) {
+            units = 0;
+            if (s0 + lane < last) {
+                load_sequence<ROWS>(a, mine, s0 + lane);
+                units = sequence_units<ROWS>(a, mine) * heads;
+            }
+            incl = before + warp_scan(units);
+            begin = incl - units;
+            const unsigned owner = __ballot_sync(0xffffffffu, begin <= r.at && r.at < incl);
+            if (owner) {
+                src = __ffs(owner) - 1;
+                w.b = s0 + src;
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    w.first = __shfl_sync(0xffffffffu, mine.first, src);
+    w.count = __shfl_sync(0xffffffffu, mine.count, src);
+    w.pos0 = __shfl_sync(0xffffffffu, mine.pos0, src);
+    w.row_tiles = __shfl_sync(0xffffffffu, mine.row_tiles, src);
+    int64_t off = r.at - __shfl_sync(0xffffffffu, begin, src);
+#pragma unroll 1
+    for (w.rt = 0;; ++w.rt) {
+        w.t = row_tile<ROWS>(a, w.count, w.pos0, w.rt);
+        const int64_t n = static_cast<int64_t>(w.t.tiles) * w.t.cost * heads;
+        if (off < n) break;
+        off -= n;
+    }
+    const int pair = w.t.tiles * w.t.cost;  // units of a pair: below 2^27
+    if (off < (int64_t(1) << 31)) {
+        w.h = static_cast<int>(off) / pair;
+        w.tile = static_cast<int>(off) - w.h * pair;
+    } else {
+        w.h = static_cast<int>(off / pair);
+        w.tile = static_cast<int>(off % pair);
+    }
+    if (ROWS > 32 && w.t.cost == 2) {
+        // a tile belongs to the CTA that its first unit falls to
+        r.at += w.tile & 1;
+        w.tile = (w.tile + 1) >> 1;
+        if (w.tile == w.t.tiles && r.at < r.end) next_pair<ROWS>(a, w);
+    }
+    return r;
+}
 
 // Tiles of the walk's pair that begin within the next `units`.
 template <int ROWS>
