@@ -992,7 +992,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                 }
             }
         }
-    compute_sync();  // the statistics are read
+    compute_sync();  // the statistics and the last share are read
 }
 
 template <int DT, bool QF32, int DP, int ROWS>
@@ -1075,7 +1075,8 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
         }
         if (w.tile == 0 && !whole) {  // the pair begins here and goes on in the next CTAs
             // (a tile belongs to the CTA that its first unit falls to)
-            join = make_int4(r.owner(at + static_cast<int64_t>(w.t.tiles - 1) * w.t.cost), 2 * w.t.rows + slot, w.first * a.group + w.t.first_row, w.h);
+            const int last = r.owner(at + static_cast<int64_t>(w.t.tiles - 1) * w.t.cost);
+            join = make_int4(last, 2 * w.t.rows + slot, w.first * a.group + w.t.first_row, w.h);
         }
         at += nt * w.t.cost;
         w.tile += nt;
