@@ -436,8 +436,9 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * in elements between tokens, whole 16-byte units; out may be q itself.  scale >
  * 0 and finite.
  * Scores, statistics and sums are fp32; the probabilities carry at least 16
- * significant bits (fp32 output: 22) into the product with the values.  The
- * results do not depend on which other sequences share the step in more than
+ * significant bits (fp32 output: 22) into the product with the values -- over an
+ * fp16 cache those above 2^-34 (2^-28) of the row's largest do, and smaller ones err
+ * by at most 2^-51 of the largest.  The results do not depend on which other sequences share the step in more than
  * the order of fp32 additions, and are the same on every run.  What the cache
  * holds in places a row does not see never reaches it, NaN and infinities
  * included.  A page number outside [0, num_pages) within a sequence's length

@@ -82,6 +82,18 @@ struct FastDiv {
 #endif
 };
 
+// Attention weights are 2^(score - reference), where the reference is the row's largest
+// score (in log2 units) less this shift: the range that the cache's type leaves free.
+constexpr int kv_weight_shift(int dtype) { return dtype == MNB_F16 ? 15 : 0; }
+
+#ifdef __CUDACC__
+// Natural log-sum-exp of a row from its reference and its sum of weights.
+__device__ __forceinline__ float kv_log_sum(float reference, float sum, int shift) {
+    if (sum == 0.f) return -INFINITY;
+    return (reference + shift + log2f(ldexpf(sum, -shift))) * 0.6931471805599453f;
+}
+#endif
+
 struct KvAttnArgs {
     KvCache cache;
     KvStep step;
@@ -97,7 +109,7 @@ struct KvAttnArgs {
     int box_rows;
     // partial results of the pairs split over CTAs: two slots per CTA
     float* part_o;     // [2 * ctas][rows][padded dim]
-    float2* part_ml;   // [2 * ctas][rows]: running maximum (log2 units), sum
+    float2* part_ml;   // [2 * ctas][rows]: reference, sum of weights
     // [ctas]: the pair that begins in this CTA and goes on in later ones: {last CTA (-1: no such
     // pair), 2 * rows + slot of its part here, first flat row (token * group + head in group), key-value head}
     int4* join;

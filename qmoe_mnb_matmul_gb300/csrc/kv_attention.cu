@@ -49,7 +49,7 @@ __device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, i
     }
     if (a.lse && d == 0)
         a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            kv_log_sum(m, l, kv_weight_shift(a.cache.dtype));
 }
 
 template <int DP>

@@ -38,16 +38,21 @@
 // in 16-bit parts (3 bf16 or 2 fp16 parts: 24 / 22 bits).  P is split
 // likewise: for an fp32 output in 3 bf16 or 2 fp16 parts, for a 16-bit output
 // in 2 parts of that type, so that the error of a single rounding of P (as
-// large as that of the rounded output) does not add to it.  The MMAs of a
-// tile start from zero and are added to the running fp32 sum outside, because
-// the tensor core's own accumulation truncates: over a long cache that would
-// drift.
+// large as that of the rounded output) does not add to it.  fp16 ends at 2^-24,
+// but a row's output may be made of weights far below its largest one (a first
+// token that draws the attention and has a value near zero).  So fp16 weights are
+// 2^15 times as large (the reference lies 15 below the largest score in log2 units; 2^15
+// is exact in fp16), and their second part is multiplied by 2^11 and summed apart:
+// a weight w of the row's largest so far keeps 22 bits down to w = 2^-28, 16 down to
+// 2^-34, and errs by 2^-51 of the largest below.  The MMAs of a tile start from zero
+// and are added to the running fp32 sum outside, because the tensor core's own
+// accumulation truncates: over a long cache that would drift.
 //
 // Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens,
 // 16 query heads over 8, 1.09 GB: 173 us, 6.3 TB/s; one sequence of 131072 tokens, 32
 // over 4, 268 MB: 50 us; 777 tokens: 7.1 us, all latency (finding the range 1.5, the
 // first tile 2.5, the join 2).  16 sequences with 1 .. 5 drafts, 24 .. 40 rows, 294 MB:
-// 79 us, bound by the latency of the matrix instructions (two compute warps per
+// 82 us in fp16 (79 without the second part's own sum), bound by the latency of the matrix instructions (two compute warps per
 // scheduler, tensor pipe 33 % busy).  What was slower: rows on the instructions' long
 // side (187 us for the batch), one producer warp for keys and values (219), a page
 // lookup that a tile waits for (344).
@@ -74,6 +79,8 @@ struct Int {
 // 16-bit parts of a query and of an attention weight.
 constexpr int query_parts(int dt, bool qf32) { return !qf32 ? 1 : dt == kBF16 ? 3 : 2; }
 constexpr int weight_parts(int dt, bool qf32) { return !qf32 ? 2 : dt == kBF16 ? 3 : 2; }
+// What the second fp16 part of an attention weight is multiplied by (see "Rounding" above).
+constexpr int kF16Up = 1 << 11;
 
 // Shared-memory plan of an instantiation for row tiles of up to ROWS rows.
 template <int DP, int ROWS, bool QF32, int PARTS_Q>
@@ -124,16 +131,17 @@ template <> struct Half2<kBF16> {
     }
 };
 
-// The pair (a, b) in PARTS 16-bit parts: each the rounding of what the parts before it left.
-template <int DT, int PARTS>
+// The pair (a, b) in PARTS 16-bit parts: each the rounding of what the parts before it
+// left, times UP for each part before it.
+template <int DT, int PARTS, int UP = 1>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&out)[PARTS]) {
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
         out[p] = Half2<DT>::pack(a, b);
         if (p + 1 < PARTS) {
             const float2 h = Half2<DT>::unpack(out[p]);
-            a -= h.x;
-            b -= h.y;
+            a = (a - h.x) * UP;
+            b = (b - h.y) * UP;
         }
     }
 }
@@ -423,8 +431,8 @@ struct Smem {
     uint8_t* q;
     float* merge;
     uint64_t *k_full, *k_empty, *v_full, *v_empty;
-    float2* stats;    // [4][16]: a warp's running maximum and sum of its rows
-    float2* rows;     // [64]: the rows' maximum and sum after the join
+    float2* stats;    // [4][16]: a warp's reference and sum of its rows
+    float2* rows;     // [64]: the rows' reference and sum after the join
     float* row_unit;  // [64]: power of two that a row of fp32 queries was scaled down by
 };
 
@@ -541,6 +549,8 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     const int dim = a.cache.dim;
     const int row0 = wr * 8 * RG;  // the warp's first row of the row tile
     const float scale2 = a.scale * 1.4426950408889634f;  // scores to log2 units
+    constexpr int kShift = kv_weight_shift(DT);
+    constexpr int kUp = DT == kF16 ? kF16Up : 1;  // of the weights' second part, which is then summed apart
 
     // ---- queries: lane holds columns 2 qc, 2 qc + 1 (+ 8) of row quad of each eight
     uint32_t qf[P::kQSmem ? 1 : KS][P::kQSmem ? 1 : RG][2];
@@ -637,7 +647,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     }
 
     float o[ND][RG][4];  // columns quad, quad + 8 of each sixteen; rows 2 qc, 2 qc + 1 of each eight
-    float m[RG][2], l[RG][2];
+    float m[RG][2], l[RG][2];  // weights so far are 2^(score - m), l their sum
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
 #pragma unroll
@@ -768,14 +778,16 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
             float ref[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float big = m[g][x];
+                float big = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < MT; ++t) big = fmaxf(big, fmaxf(s[t][g][x], s[t][g][2 + x]));
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
+                // rounded up, so that no weight passes 2^shift
+                big = fmaxf(m[g][x], __fmaf_ru(big, c[g][x], -kShift));
                 // a row that has seen nothing yet keeps a zero reference, so that its exponentials are 2^-inf = 0
-                ref[x] = big == -INFINITY ? 0.f : big * c[g][x];
-                f[g][x] = exp2_approx(fmaf(m[g][x], c[g][x], -ref[x]));
+                ref[x] = big == -INFINITY ? 0.f : big;
+                f[g][x] = exp2_approx(m[g][x] - ref[x]);
                 m[g][x] = big;
             }
             float sum[2] = {0.f, 0.f};
@@ -789,7 +801,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     uint32_t parts[PP];
-                    split<DT, PP>(s[t][g][2 * y], s[t][g][2 * y + 1], parts);
+                    split<DT, PP, kUp>(s[t][g][2 * y], s[t][g][2 * y + 1], parts);
 #pragma unroll
                     for (int p = 0; p < PP; ++p) pb[t][g][p][y] = transpose8(parts[p]);
                 }
@@ -878,21 +890,21 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     load_v(n, va[n & 1]);
                 else if (n + 1 < ND)
                     load_v(n + 1, va[(n + 1) & 1]);
-                float z[RG][4];
-#pragma unroll
-                for (int g = 0; g < RG; ++g)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) z[g][x] = 0.f;
+                float z[kUp > 1 ? PP : 1][RG][4] = {};
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
-                        for (int g = 0; g < RG; ++g) mma<DT>(z[g], va[n & 1][t], pb[t][g][p][0], pb[t][g][p][1]);
+                        for (int g = 0; g < RG; ++g)
+                            mma<DT>(z[kUp > 1 ? p : 0][g], va[n & 1][t], pb[t][g][p][0], pb[t][g][p][1]);
 #pragma unroll
                 for (int g = 0; g < RG; ++g)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) o[n][g][x] = fmaf(o[n][g][x], f[g][x & 1], z[g][x]);
+                    for (int x = 0; x < 4; ++x) {
+                        if constexpr (kUp > 1) z[0][g][x] = fmaf(z[1][g][x], 1.f / kUp, z[0][g][x]);
+                        o[n][g][x] = fmaf(o[n][g][x], f[g][x & 1], z[0][g][x]);
+                    }
             }
         }
         if (edge) fence_proxy_async_smem();  // cleared values, before the slot's next copy
@@ -901,14 +913,13 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     }
 
     // ---- end of the pair's part in this CTA: the warps that share rows agree on
-    // their maximum (in log2 units) and sum, and scale to it
+    // their reference and sum, and scale to it
 #pragma unroll
     for (int g = 0; g < RG; ++g)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) l[g][x] += __shfl_xor_sync(0xffffffffu, l[g][x], y);
-            m[g][x] *= c[g][x];
             if (quad == 0) sm.stats[warp * 16 + g * 8 + qc * 2 + x] = make_float2(m[g][x], l[g][x]);
         }
     compute_sync();
@@ -984,7 +995,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     }
                     if (a.lse && d == 0)
                         a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-                            ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+                            kv_log_sum(ml.x, ml.y, kShift);
                 } else {
                     const int64_t at = static_cast<int64_t>(part) * ROWS + rr;
                     *reinterpret_cast<float4*>(a.part_o + at * DP + d) = sum;
