@@ -607,10 +607,11 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     for (int i = 0; i < PL; ++i) big = fmaxf(big, fmaxf(fabsf(v[k][i].x), fabsf(v[k][i].y)));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    // 2^-e and 2^e of the largest magnitude's exponent, for normal numbers
-                    // of moderate size; others keep their scale
-                    const uint32_t e = __float_as_uint(big) >> 23;
-                    if (e > 27 && e < 227) {
+                    // 2^-e and 2^e of the largest magnitude's exponent, as far as both are
+                    // normal numbers; a row with an infinity keeps its scale
+                    uint32_t e = __float_as_uint(big) >> 23;
+                    if (e < 255u) {
+                        e = min(max(e, 1u), 253u);
                         down = __uint_as_float((254u - e) << 23);
                         up = __uint_as_float(e << 23);
                     }
@@ -642,7 +643,11 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
 #pragma unroll
             for (int g = 0; g < RG; ++g)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) c[g][x] *= sm.row_unit[row0 + g * 8 + qc * 2 + x];
+                for (int x = 0; x < 2; ++x) {
+                    // never 0 or infinite: a score of -inf (unseen) or 0 times it stays what it is
+                    const float k = c[g][x] * sm.row_unit[row0 + g * 8 + qc * 2 + x];
+                    c[g][x] = fminf(fmaxf(k, __uint_as_float(1u)), 3.402823466e38f);
+                }
         }
     }
 

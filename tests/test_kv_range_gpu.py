@@ -81,3 +81,19 @@ def test_spread_weights_below_a_sink(cache, dtype, group, new):
     q = q.to(DT[dtype])
     out, lse = run(bt, q, scale=1.0)
     check(bt, q, out, lse, group, 1.0, 0, dtype)
+
+
+@pytest.mark.parametrize("cache", ["f16", "bf16"])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("scale,spread", [(1e-30, 1e-16), (1e-38, 1e-30), (2.0 ** -149, 1.0), (1e-31, 1e31), (1e-37, 1e37),
+                                          (1e31, 1e-31), (1e36, 1e-37), (1e3, 1e-41)])
+def test_queries_and_scales_of_any_magnitude(cache, group, new, scale, spread):
+    """fp32 queries far from 1 with a scale that brings the scores back, or that leaves nothing of them (all weights
+    equal)."""
+    g = rng("magnitude", cache, group, new, scale, spread)
+    bt = Batch(g, [300, 65, 1], [new, new, 1], 2, 128, 16, cache)
+    bt.fill(g)
+    q = torch.randn((bt.tokens, 2 * group, 128), generator=g, device="cuda") * spread
+    q[0, 0] = 0.0
+    out, lse = run(bt, q, scale=scale)
+    check(bt, q, out, lse, group, float(torch.tensor(scale)), 0, "f32")
