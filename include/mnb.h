@@ -435,13 +435,15 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * q, out [tokens, q_heads, head_dim] in dtype (f32 or the cache's) with strides
  * in elements between tokens, whole 16-byte units; out may be q itself.  scale >
  * 0 and finite.
- * Scores, statistics and sums are fp32; the probabilities carry at least 16
+ * Scores, statistics and sums are fp32; fp32 queries carry 24 significant bits
+ * into their products (over an fp16 cache 22, elements below 2^-17 of the row's
+ * largest an error of 2^-39 of it).  The probabilities carry at least 16
  * significant bits (fp32 output: 22) into the product with the values -- over an
  * fp16 cache those above 2^-34 (2^-28) of the row's largest do, and smaller ones err
- * by at most 2^-51 of the largest.  The results do not depend on which other sequences share the step in more than
- * the order of fp32 additions, and are the same on every run.  What the cache
- * holds in places a row does not see never reaches it, NaN and infinities
- * included.  A page number outside [0, num_pages) within a sequence's length
+ * by at most 2^-51 of the largest.  The results do not depend on which other
+ * sequences share the step in more than the order of fp32 additions, and are the
+ * same on every run.  What the cache holds in places a row does not see never
+ * reaches it, NaN and infinities included.  A page number outside [0, num_pages) within a sequence's length
  * reads as zeros and records MNB_ERR_CONTENT; a length past max_pages *
  * page_size is cut there.
  * Made for a few new tokens per sequence (decoding, drafts): one pass over the

@@ -35,7 +35,8 @@
 //
 // Rounding.  K and V are exact 16-bit operands.  Queries of the cache's type go
 // in as they are; fp32 queries are scaled by a power of two per row and split
-// in 16-bit parts (3 bf16 or 2 fp16 parts: 24 / 22 bits).  P is split
+// in 16-bit parts (3 bf16 or 2 fp16 parts: 24 / 22 bits; fp16: of elements down to
+// 2^-17 of the row's largest, smaller ones err by 2^-39 of it).  P is split
 // likewise: for an fp32 output in 3 bf16 or 2 fp16 parts, for a 16-bit output
 // in 2 parts of that type, so that the error of a single rounding of P (as
 // large as that of the rounded output) does not add to it.  fp16 ends at 2^-24,
@@ -579,7 +580,10 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
         compute_sync();  // the queries of the pair before are read
         if constexpr (QF32) {
             // a warp takes every fourth row, several at a time so that their loads overlap;
-            // rows are scaled to a largest magnitude in [1, 2)
+            // rows are scaled to a largest magnitude in [1, 2), over an fp16 cache in [2^14,
+            // 2^15): the second fp16 part ends at 2^-24, and a row may have one element that
+            // dwarfs the others and meets keys near zero
+            constexpr uint32_t kUpBy = DT == kF16 ? 14 : 0;
             constexpr int PL = (DP + 63) / 64;  // element pairs per lane
             constexpr int MINE = 2 * RG * WR, AT_ONCE = MINE < 4 ? MINE : 4;
 #pragma unroll 1
@@ -607,11 +611,11 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     for (int i = 0; i < PL; ++i) big = fmaxf(big, fmaxf(fabsf(v[k][i].x), fabsf(v[k][i].y)));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    // 2^-e and 2^e of the largest magnitude's exponent, as far as both are
-                    // normal numbers; a row with an infinity keeps its scale
+                    // 2^(kUpBy - e) and 2^(e - kUpBy) of the largest magnitude's exponent, as
+                    // far as both are normal numbers; a row with an infinity keeps its scale
                     uint32_t e = __float_as_uint(big) >> 23;
                     if (e < 255u) {
-                        e = min(max(e, 1u), 253u);
+                        e = min(max(e, kUpBy + 1u), kUpBy + 253u) - kUpBy;
                         down = __uint_as_float((254u - e) << 23);
                         up = __uint_as_float(e << 23);
                     }

@@ -97,3 +97,20 @@ def test_queries_and_scales_of_any_magnitude(cache, group, new, scale, spread):
     q[0, 0] = 0.0
     out, lse = run(bt, q, scale=scale)
     check(bt, q, out, lse, group, float(torch.tensor(scale)), 0, "f32")
+
+
+@pytest.mark.parametrize("cache", ["f16", "bf16"])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("ratio", [2.0 ** 8, 2.0 ** 12, 2.0 ** 16])
+def test_a_query_element_that_dwarfs_the_others(cache, group, new, ratio):
+    """The keys are zero where the query is large: the scores are made of its small elements."""
+    g = rng("outlier", cache, group, new, ratio)
+    bt = Batch(g, [300, 65], [new, new], 2, 128, 16, cache)
+    bt.fill(g)
+    for b in range(2):
+        pages = bt.table[b, :-(-bt.lens[b] // 16)].long()
+        bt.k[pages, :, :, 7] = 0
+    q = torch.randn((bt.tokens, 2 * group, 128), generator=g, device="cuda") * 2
+    q[..., 7] = 2.0 * ratio
+    out, lse = run(bt, q)
+    check(bt, q, out, lse, group, 128 ** -0.5, 0, "f32")
