@@ -444,8 +444,9 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * sequences share the step in more than the order of fp32 additions, and are the
  * same on every run.  What the cache holds in places a row does not see never
  * reaches it, NaN and infinities included.  A page number outside [0, num_pages) within a sequence's length
- * reads as zeros and records MNB_ERR_CONTENT; a length past max_pages *
- * page_size is cut there.
+ * reads as zeros and records MNB_ERR_CONTENT.  So does a length past max_pages *
+ * page_size: the new tokens keep their positions, and see those of their tokens
+ * that have a page.
  * Made for a few new tokens per sequence (decoding, drafts): one pass over the
  * cache serves 64 rows, so that a prompt is right but re-reads it.  workspace
  * 256-byte aligned. */

@@ -25,8 +25,9 @@ struct KvStep {
     const int* page_table;  // [batch, max_pages], rows table_stride apart
     int64_t table_stride;
     int batch, tokens, max_pages;
-    int capacity;           // min(max_pages * page_size, 2^31 - 1)
+    int capacity;           // min(max_pages * page_size, kKvMaxCapacity)
 };
+constexpr int kKvMaxCapacity = 0x7fffffff - 4096;  // positions are 32-bit, with room for a tile past the end
 
 // First new token and number of new tokens of sequence b, kept inside
 // [0, tokens] whatever new_start holds.

@@ -72,8 +72,7 @@ mnb_status check_step(const kv_step_desc* d, const KvCache& c, KvStep* s, bool* 
     s->tokens = d->tokens;
     s->max_pages = d->max_pages;
     const int64_t cap = int64_t(d->max_pages) * c.page_size;
-    // positions are 32-bit, with room for a tile past the end
-    s->capacity = static_cast<int>(cap < kMaxInt - 4096 ? cap : kMaxInt - 4096);
+    s->capacity = static_cast<int>(cap < kKvMaxCapacity ? cap : kKvMaxCapacity);
     return MNB_OK;
 }
 
@@ -186,7 +185,7 @@ mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, co
     a.out_stride = out_stride;
     a.lse = lse;
     a.scale = scale;
-    a.window = static_cast<int>(window < a.step.capacity ? window : 0);  // a window as wide as the cache masks nothing
+    a.window = static_cast<int>(window <= kMaxInt ? window : 0);  // positions are 32-bit: a wider one masks nothing
     const int sms = sm_count_current();
     if (sms <= 0) return MNB_ERR_CUDA;
     return from_cuda(launch_kv_attention(a, dtype, step->max_new, workspace, sms, pdl_enabled(),

@@ -243,9 +243,10 @@ struct Walk {
     RowTile t;
 };
 
-// The first token that the row at position pos sees (window 0: every earlier one).
-__device__ __forceinline__ int window_start(int window, int pos) {
-    return window > 0 && pos >= window ? pos + 1 - window : 0;
+// The first token that the row at position pos sees (window 0: every earlier one);
+// the capacity where it sees none of the tokens that have a page.
+__device__ __forceinline__ int window_start(const KvAttnArgs& a, int pos) {
+    return a.window > 0 && pos >= a.window ? min(pos + 1 - a.window, a.step.capacity) : 0;
 }
 
 template <int ROWS>
@@ -258,8 +259,8 @@ __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int 
     const int cap = a.step.capacity;
     t.hi = min(max(pos0 + tok1 + 1, 0), cap);
     t.hi_all = min(max(pos0 + tok0 + 1, 0), cap);
-    t.lo = window_start(a.window, pos0 + tok0);
-    t.lo_all = window_start(a.window, pos0 + tok1);
+    t.lo = window_start(a, pos0 + tok0);
+    t.lo_all = window_start(a, pos0 + tok1);
     // a tile of more than 32 rows takes about twice the time of one that HBM bounds
     // (its matrix instructions bound it: measured 4900 against 2700 cycles)
     t.cost = ROWS > 32 && t.rows > 32 ? 2 : 1;
@@ -271,8 +272,9 @@ __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int 
 template <int ROWS>
 __device__ __forceinline__ void load_sequence(const KvAttnArgs& a, Walk& w, int seq) {
     w.b = seq;
-    // a length beyond the page table is cut there (kv_append records it)
-    const int len = min(__ldg(a.step.seq_lens + seq), a.step.capacity);
+    // (beyond the page table the new tokens keep their positions, and rows see the tokens
+    // that have a page; beyond any page table, there is no room for sums of positions)
+    const int len = min(__ldg(a.step.seq_lens + seq), kKvMaxCapacity);
     step_tokens(a.step, seq, &w.first, &w.count);
     w.pos0 = max(len, 0) - w.count;
     w.row_tiles = (w.count * a.group + ROWS - 1) / ROWS;
@@ -490,6 +492,7 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
     bool ok = true, bad = false;
     while (at < r.end && ok) {
         const int nt = part_tiles<ROWS>(w, r.end - at);
+        bad = bad || w.pos0 + w.count > a.step.capacity;
         int tok = (w.t.lo / kKvTile + w.tile) * kKvTile + row0;
         // page and row of the box at token tok; boxes that no row sees are asked for
         // outside the cache, which fills them with zeros and reads nothing
@@ -522,7 +525,8 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
         w.tile += nt;
         if (at < r.end) next_pair<ROWS>(a, w);
     }
-    if (bad) record_error(MNB_ERR_CONTENT);  // a page number outside the cache: its tokens read as zeros
+    // a page number outside the cache: its tokens read as zeros; or a length past the page table
+    if (bad) record_error(MNB_ERR_CONTENT);
     // no copy may be in flight when the CTA ends, whatever the compute warps
     // waited for: see the copies of the last slots land
     for (int n = max(0, issued - SLOTS); n < issued; ++n)
@@ -678,7 +682,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     auto sees = [&](int rr, int& lo, int& hi) {
         const int pos = w.pos0 + a.by_group(w.t.first_row + rr);
         hi = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
-        lo = window_start(a.window, pos);
+        lo = window_start(a, pos);
     };
 
 #pragma unroll 1

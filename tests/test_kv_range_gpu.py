@@ -114,3 +114,39 @@ def test_a_query_element_that_dwarfs_the_others(cache, group, new, ratio):
     q[..., 7] = 2.0 * ratio
     out, lse = run(bt, q)
     check(bt, q, out, lse, group, 128 ** -0.5, 0, "f32")
+
+
+def past_the_table(g, cache, group, new, window, dtype):
+    """Two sequences, the first longer than its page table of 7 pages of 16 tokens."""
+    bt = Batch(g, [112, 70], [new, new], 2, 64, 16, cache)
+    bt.fill(g)
+    bt.seq_lens[0] = 112 + new - 1 if new > 1 else 112 + 5
+    q = torch.randn((bt.tokens, 2 * group, 64), generator=g, device="cuda").to(DT[dtype])
+    out, lse = run(bt, q, window=window, error=CONTENT)
+    length, out64 = int(bt.seq_lens[0]), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    V = torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    for i in range(new):
+        pos = length - new + i
+        lo, hi = (max(0, pos + 1 - window) if window else 0), min(pos + 1, 112)
+        for h in range(2 * group):
+            k, v = bt.rows_of(0, h // group)
+            if lo < hi:
+                p = torch.softmax(q[i, h].double() @ k[lo:hi].T / 8, -1)
+                out64[i, h], V[i, h] = p @ v[lo:hi], (p @ v[lo:hi].abs()).max()
+            assert bool(torch.isfinite(lse[i, h])) == (lo < hi)
+    tol = HALF_ULP[dtype] * out64[:new].abs() + (V[:new] * 2.0 ** -12)[..., None] + TINY[dtype]
+    assert bool(((out[:new].double() - out64[:new]).abs() <= tol).all())
+    # the other sequence is as always
+    bt.seq_lens[0] = 112
+    again, _ = run(bt, q, window=window)
+    check(bt, q, again, None, group, 0.125, window, dtype)
+    assert torch.equal(again[new:], out[new:])
+
+
+@pytest.mark.parametrize("cache,dtype", [("f16", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("group,new", [(2, 1), (2, 4), (8, 3), (8, 6), (3, 40)])
+@pytest.mark.parametrize("window", [0, 3, 50, 112, 120])
+def test_a_length_past_the_page_table(cache, dtype, group, new, window):
+    """New tokens keep their positions, and with them what they see of the tokens that have a page; the length is
+    reported."""
+    past_the_table(rng("past", cache, dtype, group, new, window), cache, group, new, window, dtype)
