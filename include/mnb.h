@@ -443,7 +443,8 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * by at most 2^-51 of the largest.  The results do not depend on which other
  * sequences share the step in more than the order of fp32 additions, and are the
  * same on every run.  What the cache holds in places a row does not see never
- * reaches it, NaN and infinities included.  A page number outside [0, num_pages) within a sequence's length
+ * reaches it, NaN and infinities included; an infinite value in a place that it
+ * sees gives that infinity, opposite ones or a NaN give NaN.  A page number outside [0, num_pages) within a sequence's length
  * reads as zeros and records MNB_ERR_CONTENT.  So does a length past max_pages *
  * page_size: the new tokens keep their positions, and see those of their tokens
  * that have a page.

@@ -52,6 +52,13 @@ __device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, i
             kv_log_sum(m, l, kv_weight_shift(a.cache.dtype));
 }
 
+// A part's weight.  Never zero: a part with an infinite column adds that infinity
+// however small its weight (2^-126 of anything finite changes nothing).
+__device__ __forceinline__ float part_weight(float reference, float largest) {
+    const float w = exp2f(reference - largest);
+    return w < 1.17549435e-38f ? 1.17549435e-38f : w;  // (NaN stays NaN)
+}
+
 template <int DP>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int rows_per_tile, int out_dtype) {
     constexpr int NV = DP / 64;    // float2 per lane
@@ -76,7 +83,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
             float m = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float w = lane < n ? exp2f(ml.x - (m == -INFINITY ? 0.f : m)) : 0.f;
+            const float w = lane < n ? part_weight(ml.x, m == -INFINITY ? 0.f : m) : 0.f;
             const float l = warp_sum(w * ml.y);
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
         for (int x = 0; x < 3; ++x) {
             const int i = threadIdx.x + 128 * x;
             if (i >= n) continue;
-            const float w = exp2f(ml[x].x - ref);
+            const float w = part_weight(ml[x].x, ref);
             weight[i] = w;
             l = fmaf(w, ml[x].y, l);
         }

@@ -533,11 +533,81 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
         warp_wait(&full[n % SLOTS], static_cast<uint32_t>(n / SLOTS) & 1u);
 }
 
+// Tokens [lo, hi) that row rr of the row tile sees.
+__device__ __forceinline__ void row_sees(const KvAttnArgs& a, const Walk& w, int rr, int& lo, int& hi) {
+    const int pos = w.pos0 + a.by_group(w.t.first_row + rr);
+    hi = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
+    lo = window_start(a, pos);
+}
+
+// Where the result of a part is stored: share (g, half) of the merge takes eight rows of
+// each of WR row groups (RG eights each) and half the columns, and step k of a share
+// gives this thread four columns of one row.
+struct Place {
+    int rr, d;  // row of the row tile, first of the four columns
+};
+template <int DP>
+__device__ __forceinline__ Place merge_place(int rg, int g, int half, int k) {
+    constexpr int HALF = DP / 2, V4 = HALF / 4;
+    const int i = threadIdx.x + 32 * kComputeWarps * k;
+    return {i / (8 * V4) * 8 * rg + g * 8 + i / V4 % 8, half * HALF + i % V4 * 4};
+}
+
+// An infinite value that a row sees gives that infinity, a NaN or opposite infinities
+// NaN: every weight is positive, though fp32 or a weight's smaller parts may hold it
+// as zero, which makes NaN of an infinity in the products.  So where a part came out
+// with columns that are not finite (bits of `odd`: share 8 * (2 g + half) + step), each
+// of them is looked through once more and gets the sum of its values that are not
+// finite (if there are none, fp32 did not hold the sum, and it stays).  Looking at each
+// stored result costs 0.1 us of a short call (7.1 us of 777 tokens).
+template <int DT, bool QF32, int DP, int ROWS>
+__device__ __forceinline__ void odd_columns(const KvAttnArgs& a, const Smem& sm, const Walk& w, int nt, bool whole,
+                                            int part, int rg, uint32_t odd) {
+    using H = Half2<DT>;
+    const int from = (w.t.lo / kKvTile + w.tile) * kKvTile;
+    const int* pages = a.step.page_table + w.b * a.step.table_stride;
+#pragma unroll 1
+    for (; odd != 0; odd &= odd - 1) {
+        const int bit = __ffs(odd) - 1;
+        const Place at = merge_place<DP>(rg, bit >> 4, bit >> 3 & 1, bit & 7);
+        if (at.d >= a.cache.dim || sm.rows[at.rr].y != sm.rows[at.rr].y) continue;  // (NaN: among the scores)
+        int lo, hi;
+        row_sees(a, w, at.rr, lo, hi);
+        hi = min(hi, from + nt * kKvTile);
+        const uint16_t* values = static_cast<const uint16_t*>(a.cache.v) + w.h * a.cache.head_stride + at.d;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int j = max(lo, from); j < hi; ++j) {
+            const int index = a.by_page(j), page = __ldg(pages + index);
+            if (page < 0 || page >= a.cache.num_pages) continue;
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(
+                values + page * a.cache.page_stride + (j - index * a.cache.page_size) * a.cache.token_stride));
+            const float2 v0 = H::unpack(x.x & H::odd(x.x)), v1 = H::unpack(x.y & H::odd(x.y));
+            sum[0] += v0.x;
+            sum[1] += v0.y;
+            sum[2] += v1.x;
+            sum[3] += v1.y;
+        }
+        const int flat = w.t.first_row + at.rr, tok = a.by_group(flat);
+        const int64_t off = (w.first + tok) * a.out_stride +
+                            static_cast<int64_t>(w.h * a.group + flat - tok * a.group) * a.cache.dim + at.d;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (sum[x] == 0.f) continue;
+            if (!whole)
+                a.part_o[(static_cast<int64_t>(part) * ROWS + at.rr) * DP + at.d + x] = sum[x];
+            else
+                store_from_f32(a.out, QF32 ? kF32 : DT, off + x, sum[x]);
+        }
+    }
+}
+
 // One pair's tiles w.tile .. w.tile + nt - 1 by the four compute warps, WR of them
 // along the rows (8 RG rows each) and 4 / WR along a tile's tokens; the result goes
-// to the output (`whole`) or to slot `part` of the workspace.
+// to the output (`whole`) or to slot `part` of the workspace.  Returns where this
+// thread's share of it is not finite (see odd_columns).
 template <int DT, bool QF32, int DP, int ROWS, int WR, int RG, int KSLOTS, int VSLOTS>
-__device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, const Walk& w, int nt, bool whole, int part,
+__device__ __forceinline__ uint32_t run_part(const KvAttnArgs& a, const Smem& sm, const Walk& w, int nt, bool whole, int part,
                                          Ring<KSLOTS>& kring, Ring<VSLOTS>& vring, bool& ok) {
     constexpr int PQ = query_parts(DT, QF32), PP = weight_parts(DT, QF32);
     using P = Plan<DP, ROWS, QF32, PQ>;
@@ -678,13 +748,6 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     const uint32_t k_lane = tile_at(kKvTile, wt * TOK + (lane & 15), lane >> 4);
     const uint32_t v_lane = tile_at(kKvTile, wt * TOK + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
     const uint32_t q_lane = smem_u32(sm.q) + tile_at(ROWS, row0 + (lane & 7), lane >> 3);
-    // tokens [lo, hi) that row `rr` of the row tile sees
-    auto sees = [&](int rr, int& lo, int& hi) {
-        const int pos = w.pos0 + a.by_group(w.t.first_row + rr);
-        hi = rr < w.t.rows ? min(pos + 1, a.step.capacity) : 0;
-        lo = window_start(a, pos);
-    };
-
 #pragma unroll 1
     for (int i = 0; i < nt; ++i, tok0 += kKvTile) {
         // tokens that not every row sees
@@ -774,7 +837,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     int lo, hi;
-                    sees(row0 + g * 8 + qc * 2 + x, lo, hi);
+                    row_sees(a, w, row0 + g * 8 + qc * 2 + x, lo, hi);
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -857,7 +920,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                 for (int g = 0; g < RG; ++g) {
                     int lo[2], hi[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) sees(row0 + g * 8 + qc * 2 + x, lo[x], hi[x]);
+                    for (int x = 0; x < 2; ++x) row_sees(a, w, row0 + g * 8 + qc * 2 + x, lo[x], hi[x]);
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
                         float add[4] = {0.f, 0.f, 0.f, 0.f};
@@ -963,7 +1026,9 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
     // contiguous.  (Rolled loops: this runs once or twice in a launch, so that the
     // fetch of its instructions counts.  Written from the accumulators, unrolled, it
     // made a short call 0.5 us slower.)
-    constexpr int HALF = DP / 2, V4 = HALF / 4;
+    constexpr int V4 = DP / 8;  // steps of four columns in half of them
+    static_assert(V4 * WR / 16 <= 8 && RG <= 2, "the bits of `odd`");
+    uint32_t odd = 0;
 #pragma unroll
     for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -977,9 +1042,9 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     mine[(qc * 2 + (x & 1)) * P::kMergeRow + n * 16 + quad + 8 * (x >> 1)] = o[half * (ND / 2) + n][g][x];
             compute_sync();
 #pragma unroll 1
-            for (int i = threadIdx.x; i < 8 * WR * V4; i += 32 * kComputeWarps) {
+            for (int i = threadIdx.x, bit = 8 * (2 * g + half); i < 8 * WR * V4; i += 32 * kComputeWarps, ++bit) {
                 const int d4 = i % V4, r8 = i / V4 % 8, grp = i / (8 * V4);
-                const int rr = grp * 8 * RG + g * 8 + r8, d = half * HALF + d4 * 4;
+                const int rr = grp * 8 * RG + g * 8 + r8, d = half * (DP / 2) + d4 * 4;
                 if (rr >= w.t.rows) continue;
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -991,6 +1056,8 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
                     sum.z += v.z;
                     sum.w += v.w;
                 }
+                // (a sum of finite numbers that overflows is looked at for nothing)
+                if (!(fabsf((sum.x + sum.y) + (sum.z + sum.w)) <= 3.402823466e38f)) odd |= 1u << bit;
                 const float2 ml = sm.rows[rr];
                 if (whole) {
                     const int flat = w.t.first_row + rr, tok = a.by_group(flat);
@@ -1017,6 +1084,7 @@ __device__ __forceinline__ void run_part(const KvAttnArgs& a, const Smem& sm, co
             }
         }
     compute_sync();  // the statistics and the last share are read
+    return odd;
 }
 
 template <int DT, bool QF32, int DP, int ROWS>
@@ -1083,20 +1151,22 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
         const int slot = at == r.at ? 0 : 1, part = 2 * blockIdx.x + slot;  // (r.at is the first part's first unit)
         // the warps split along the rows only as far as the pair's rows need
         auto run = [&](auto wr, auto rg) {
-            run_part<DT, QF32, DP, ROWS, decltype(wr)::value, decltype(rg)::value>(a, sm, w, nt, whole, part, kring, vring,
-                                                                                  ok);
+            return run_part<DT, QF32, DP, ROWS, decltype(wr)::value, decltype(rg)::value>(a, sm, w, nt, whole, part, kring,
+                                                                                         vring, ok);
         };
+        uint32_t odd = 0;
         if (ROWS == 8 || w.t.rows <= 8) {
-            run(Int<1>{}, Int<1>{});
+            odd = run(Int<1>{}, Int<1>{});
         } else if constexpr (ROWS > 8) {
             if (w.t.rows <= 16) {
-                run(Int<1>{}, Int<2>{});
+                odd = run(Int<1>{}, Int<2>{});
             } else if (ROWS == 32 || w.t.rows <= 32) {
-                run(Int<2>{}, Int<2>{});
+                odd = run(Int<2>{}, Int<2>{});
             } else if constexpr (ROWS > 32) {
-                run(Int<4>{}, Int<2>{});
+                odd = run(Int<4>{}, Int<2>{});
             }
         }
+        if (odd) odd_columns<DT, QF32, DP, ROWS>(a, sm, w, nt, whole, part, w.t.rows <= 8 ? 1 : 2, odd);
         if (w.tile == 0 && !whole) {  // the pair begins here and goes on in the next CTAs
             // (a tile belongs to the CTA that its first unit falls to)
             const int last = r.owner(at + static_cast<int64_t>(w.t.tiles - 1) * w.t.cost);

@@ -150,3 +150,73 @@ def test_a_length_past_the_page_table(cache, dtype, group, new, window):
     """New tokens keep their positions, and with them what they see of the tokens that have a page; the length is
     reported."""
     past_the_table(rng("past", cache, dtype, group, new, window), cache, group, new, window, dtype)
+
+
+@pytest.mark.parametrize("cache,dtype", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("length,at", [(300, 10), (300, 100), (300, 290), (40001, 20000), (40001, 39990)])
+def test_an_infinite_value_gives_that_infinity(cache, dtype, group, new, length, at):
+    """Wherever the token lies in its tile and whatever its weight: a positive share of an infinity."""
+    g = rng("infinite", cache, dtype, group, new, length, at)
+    bt = Batch(g, [length, 70], [new, new], 2, 80, 16, cache)
+    bt.fill(g)
+    page, row = bt.place(0, at)
+    bt.v[page, 0, row, 5] = math.inf
+    bt.v[page, 1, row, 6] = -math.inf
+    bt.v[page, 1, row, 79] = math.nan
+    page, row = bt.place(0, 40)
+    bt.v[page, 0, row, 9] = math.inf
+    page, row = bt.place(0, 41)
+    bt.v[page, 0, row, 9] = -math.inf
+    q = (torch.randn((bt.tokens, 2 * group, 80), generator=g, device="cuda") * 2).to(DT[dtype])
+    out, lse = run(bt, q)
+    inf = torch.full((new, group), math.inf, dtype=out.dtype, device="cuda")
+    assert torch.equal(out[:new, :group, 5], inf) and torch.equal(out[:new, group:, 6], -inf)
+    assert bool(torch.isnan(out[:new, group:, 79]).all()) and bool(torch.isnan(out[:new, :group, 9]).all())
+    odd = torch.zeros_like(out, dtype=torch.bool)
+    odd[:new, :group, 5] = odd[:new, :group, 9] = odd[:new, group:, 6] = odd[:new, group:, 79] = True
+    torch.nan_to_num_(bt.v, 0.0, 0.0, 0.0)  # what is not odd is as if those values were zero
+    ref, rlse, (A, V) = reference(bt, q, group, 80 ** -0.5, 0)
+    tol = HALF_ULP[dtype] * ref.abs() + (V * 2.0 ** -12)[..., None] + TINY[dtype]
+    assert bool(((out.double() - ref).abs() <= tol)[~odd].all())
+    assert bool(((lse.double() - rlse).abs() <= 1e-3).all())
+
+
+@pytest.mark.parametrize("cache,dtype", [("f16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("lead", [0, 17000, 39000])  # before, among and after the infinite value's own part
+def test_an_infinite_value_of_a_weight_below_fp32(cache, dtype, group, new, lead):
+    """Another token leads by 200 nats: e^-200 is no fp32 number, and no zero."""
+    g = rng("faint", cache, dtype, group, new, lead)
+    bt = Batch(g, [40000], [new], 1, 64, 16, cache)
+    bt.fill(g)
+    pages = bt.table[0, :2500].long()
+    bt.k[pages, :, :, 0] = 0
+    set_token(bt, 0, lead, k=torch.nn.functional.one_hot(torch.tensor(0), 64).cuda() * 200.0)
+    page, row = bt.place(0, 20000)
+    bt.v[page, 0, row, 11] = math.inf
+    q = torch.randn((new, group, 64), generator=g, device="cuda") * 0.1
+    q[..., 0] = 1.0
+    q = q.to(DT[dtype])
+    out, _ = run(bt, q, scale=1.0)
+    assert bool((out[..., 11] == math.inf).all())
+    assert bool(torch.isfinite(out[..., :11]).all()) and bool(torch.isfinite(out[..., 12:]).all())
+
+
+def test_a_value_that_overflows_the_cache_and_a_window_past_it():
+    """fp32 values above 65504 become infinities of an fp16 cache; a window that has left them sees none."""
+    g = rng("overflow")
+    bt = Batch(g, [200], [1], 1, 64, 16, "f16", new_start=False)
+    bt.fill(g)
+    q = torch.randn((1, 2, 64), generator=g, device="cuda")
+    k, v = torch.randn((1, 1, 64), generator=g, device="cuda"), torch.ones((1, 1, 64), device="cuda")
+    v[0, 0, 3] = 1e6
+    mnb.kv_append(bt.cache, bt.step, None, k, v, None)
+    out, _ = run(bt, q)
+    assert bool((out[..., 3] == math.inf).all()) and bool(torch.isfinite(out[..., 4:]).all())
+    set_token(bt, 0, 199, v=0.0)
+    page, row = bt.place(0, 150)
+    bt.v[page, 0, row, 20] = -math.inf
+    assert bool((run(bt, q)[0][..., 20] == -math.inf).all())
+    assert bool((run(bt, q, window=50)[0][..., 20] == -math.inf).all())
+    assert bool(torch.isfinite(run(bt, q, window=49)[0][..., 20]).all())
