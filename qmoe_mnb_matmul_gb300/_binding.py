@@ -62,6 +62,7 @@ class MnbError(RuntimeError):
         self.call = call
 
 
+_address = ctypes.addressof
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
@@ -410,7 +411,7 @@ def kv_cache(k, v) -> KvCacheDesc:
         raise ValueError("the head dimension must have unit stride")
     d = KvCacheDesc(_on_gpu(k, "k"), _on_gpu(v, "v"), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[2],
                     k.shape[1], k.shape[3], _dtype_code(k))
-    d.tensors, d.ref = (k, v), ctypes.byref(d)  # kept alive with the descriptor
+    d.tensors = (k, v)  # kept alive with the descriptor
     return d
 
 
@@ -432,7 +433,7 @@ def kv_step(seq_lens, page_table, new_start=None, tokens=None, max_new=1) -> KvS
     d = KvStepDesc(_packed(seq_lens, "seq_lens", torch.int32), _packed(new_start, "new_start", torch.int32),
                    _on_gpu(page_table, "page_table", torch.int32), stride, batch, tokens, max_new,
                    page_table.shape[1])
-    d.tensors, d.ref = (seq_lens, new_start, page_table), ctypes.byref(d)
+    d.tensors = (seq_lens, new_start, page_table)
     return d
 
 
@@ -443,7 +444,7 @@ def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e
     max_pos, rot_dim = (0, 0) if cos_sin is None else cos_sin.shape
     d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32), max_pos, rot_dim, int(bool(interleaved)),
                    _packed(q_norm, "q_norm", torch.float32), _packed(k_norm, "k_norm", torch.float32), eps)
-    d.tensors, d.ref = (cos_sin, q_norm, k_norm), ctypes.byref(d)
+    d.tensors = (cos_sin, q_norm, k_norm)
     return d
 
 
@@ -491,8 +492,8 @@ def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True
         raise ValueError("q_out needs q")
     if v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    st = load_library().kv_append(cache.ref, step.ref, None if rope is None else rope.ref, qp, qs, heads, kp, ks, vp, vs,
-                                  _dtype_code(k), op, os_, _stream_of(k, stream))
+    st = load_library().kv_append(_address(cache), _address(step), None if rope is None else _address(rope), qp, qs, heads,
+                                  kp, ks, vp, vs, _dtype_code(k), op, os_, _stream_of(k, stream))
     if check:
         _check(st, "kv_append")
     return st
@@ -526,7 +527,7 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
                                 dtype=torch.uint8, device=q.device)
         if stream is not None:  # the allocation belongs to the current stream and is given back at return
             workspace.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
-    st = load_library().kv_attention(cache.ref, step.ref, qp, qs, heads, _dtype_code(q), op, os_,
+    st = load_library().kv_attention(_address(cache), _address(step), qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
                                      _packed(workspace, "workspace", None), workspace.nbytes, _stream_of(q, stream))
     if check:

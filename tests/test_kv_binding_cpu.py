@@ -1,0 +1,122 @@
+"""The binding of the paged-cache and draft-verification calls without a GPU: stand-ins
+for CUDA tensors, and a stand-in for the library that notes its calls."""
+import ctypes
+import gc
+import weakref
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import qmoe_mnb_matmul_gb300 as mnb  # noqa: E402
+from qmoe_mnb_matmul_gb300 import _binding  # noqa: E402
+
+
+class Tensor:
+    """What the binding asks of a CUDA tensor."""
+
+    def __init__(self, shape, dtype=torch.bfloat16, device=0):
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype, device
+        self.is_cuda = device >= 0
+        self._stride = torch.empty(shape, device="meta").stride()
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return 0x10000
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
+
+
+class Library:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    library = Library()
+    monkeypatch.setattr(_binding, "load_library", lambda path=None: library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+    return library
+
+
+def i32(*shape, device=0):
+    return Tensor(shape, torch.int32, device)
+
+
+def f32(*shape, device=0):
+    return Tensor(shape, torch.float32, device)
+
+
+def cache(device=0):
+    return mnb.kv_cache(Tensor((9, 2, 16, 64), device=device), Tensor((9, 2, 16, 64), device=device))
+
+
+def step(device=0):
+    return mnb.kv_step(i32(3, device=device), i32(3, 4, device=device))
+
+
+def rows(heads, device=0):
+    return Tensor((3, heads, 64), device=device)
+
+
+def append(c=None, s=None, rope=None, q=None, k=None, v=None, out=None, **kw):
+    return mnb.kv_append(c or cache(), s or step(), q or rows(4), k or rows(2), v or rows(2), out or rows(4), rope, **kw)
+
+
+def attend(c=None, s=None, q=None, out=None, ws=None, **kw):
+    return mnb.kv_attention(c or cache(), s or step(), q or rows(4), out or rows(4), ws or Tensor((1 << 20,), torch.uint8), **kw)
+
+
+@pytest.mark.parametrize("kind", ["cache", "step", "rope"])
+def test_a_dropped_descriptor_frees_its_tensors_at_once(lib, kind):
+    gc.collect()
+    gc.disable()
+    try:
+        t = {"cache": Tensor((9, 2, 16, 64)), "step": i32(3), "rope": f32(64)}[kind]
+        held = weakref.ref(t)
+        d = {"cache": lambda: mnb.kv_cache(t, t), "step": lambda: mnb.kv_step(t, i32(3, 4)),
+             "rope": lambda: mnb.kv_rope(q_norm=t)}[kind]()
+        t = None
+        assert held() is not None  # the descriptor keeps what it points to
+        d = None  # noqa: F841
+        assert held() is None
+    finally:
+        gc.enable()
+
+
+def test_a_descriptor_that_the_caller_builds(lib):
+    c = mnb.KvCacheDesc(k=0x10000, v=0x20000, num_pages=9, page_stride=2048, head_stride=1024, token_stride=64, page_size=16,
+                        kv_heads=2, head_dim=64, dtype=mnb.BF16)
+    s = mnb.KvStepDesc(seq_lens=0x10000, new_start=None, page_table=0x20000, table_stride=4, batch=3, tokens=3, max_new=1,
+                       max_pages=4)
+    r = mnb.KvRopeDesc(cos_sin=0x10000, max_pos=64, rot_dim=64, eps=1e-6)
+    append(c, s, r)
+    attend(c, s)
+    assert [name for name, _ in lib.calls] == ["kv_append", "kv_attention"]
+    at = lambda x: x if isinstance(x, int) else ctypes.cast(x, ctypes.c_void_p).value  # noqa: E731
+    assert [at(x) for x in lib.calls[0][1][:3]] == [ctypes.addressof(d) for d in (c, s, r)]
+    assert [at(x) for x in lib.calls[1][1][:2]] == [ctypes.addressof(d) for d in (c, s)]
