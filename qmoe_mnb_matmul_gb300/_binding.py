@@ -53,6 +53,7 @@ class KvRopeDesc(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
                 ("eps", ctypes.c_float)]
+    norm_dim = None  # length of the norms' weights, where kv_rope saw them
 
 
 class MnbError(RuntimeError):
@@ -442,9 +443,14 @@ def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e
     [head_dim]) of queries and keys; None leaves a part out."""
     import torch
     max_pos, rot_dim = (0, 0) if cos_sin is None else cos_sin.shape
+    lengths = {w.numel() for w in (q_norm, k_norm) if w is not None}
+    if len(lengths) > 1:
+        raise ValueError("q_norm and k_norm must have one length")
     d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32), max_pos, rot_dim, int(bool(interleaved)),
                    _packed(q_norm, "q_norm", torch.float32), _packed(k_norm, "k_norm", torch.float32), eps)
     d.tensors = (cos_sin, q_norm, k_norm)
+    if lengths:
+        d.norm_dim = lengths.pop()
     return d
 
 
@@ -492,6 +498,8 @@ def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True
         raise ValueError("q_out needs q")
     if v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
+    if rope is not None and rope.norm_dim not in (None, dim):
+        raise ValueError(f"q_norm and k_norm must have head_dim = {dim} elements, not {rope.norm_dim}")
     st = load_library().kv_append(_address(cache), _address(step), None if rope is None else _address(rope), qp, qs, heads,
                                   kp, ks, vp, vs, _dtype_code(k), op, os_, _stream_of(k, stream))
     if check:

@@ -120,3 +120,18 @@ def test_a_descriptor_that_the_caller_builds(lib):
     at = lambda x: x if isinstance(x, int) else ctypes.cast(x, ctypes.c_void_p).value  # noqa: E731
     assert [at(x) for x in lib.calls[0][1][:3]] == [ctypes.addressof(d) for d in (c, s, r)]
     assert [at(x) for x in lib.calls[1][1][:2]] == [ctypes.addressof(d) for d in (c, s)]
+
+
+def test_norms_have_one_weight_per_element_of_a_head(lib):
+    """The kernel reads head_dim (64) weights of each norm that is given."""
+    append(rope=mnb.kv_rope(q_norm=f32(64), k_norm=f32(64)))
+    append(rope=mnb.kv_rope(k_norm=f32(64)))
+    append(rope=mnb.kv_rope(f32(100, 32)))
+    assert len(lib.calls) == 3
+    for bad in (dict(q_norm=f32(32)), dict(k_norm=f32(128)), dict(q_norm=f32(32), k_norm=f32(32)), dict(k_norm=f32(0))):
+        with pytest.raises(ValueError):
+            append(rope=mnb.kv_rope(**bad))
+    for bad in (dict(q_norm=f32(64), k_norm=f32(32)), dict(q_norm=f32(32), k_norm=f32(64))):
+        with pytest.raises(ValueError):
+            append(rope=mnb.kv_rope(**bad))
+    assert len(lib.calls) == 3
