@@ -4,7 +4,8 @@ library's CUDA kernels.  There is no fallback: if the library has not been
 built, loading it raises.
 
 Tensors are torch tensors on the current CUDA device (contiguous); raw device
-pointers may be passed as ints instead.  ``stream`` is a torch.cuda.Stream, a
+pointers may be passed as ints instead (the paged-cache and draft calls take
+tensors, with strides where their text says so, and refuse those of another device).  ``stream`` is a torch.cuda.Stream, a
 raw cudaStream_t handle (int), or None for torch's current stream.
 """
 from __future__ import annotations
@@ -39,6 +40,7 @@ class KvCacheDesc(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+    device = None  # of the tensors, where kv_cache saw them
 
 
 class KvStepDesc(ctypes.Structure):
@@ -46,6 +48,7 @@ class KvStepDesc(ctypes.Structure):
     _fields_ = [("seq_lens", ctypes.c_void_p), ("new_start", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
                 ("max_new", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+    device = None
 
 
 class KvRopeDesc(ctypes.Structure):
@@ -53,6 +56,7 @@ class KvRopeDesc(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
                 ("eps", ctypes.c_float)]
+    device = None
     norm_dim = None  # length of the norms' weights, where kv_rope saw them
 
 
@@ -134,12 +138,13 @@ _DTYPE_CODES = {}
 
 
 def _dtype_code(t) -> int:
-    if not _DTYPE_CODES:
-        import torch
-        _DTYPE_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
     code = _DTYPE_CODES.get(t.dtype)
     if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
+        import torch
+        _DTYPE_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        if t.dtype not in _DTYPE_CODES:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        code = _DTYPE_CODES[t.dtype]
     return code
 
 
@@ -386,21 +391,49 @@ def qmoe_permute(topk_idx, E, counts, offsets, perm, stream=None, *, T=None, k=N
     return st
 
 
-def _on_gpu(t, name, dtype=None):
-    """The data pointer of a CUDA tensor (None stays None)."""
+def _device_of(t, name) -> int:
+    """The device of a CUDA tensor."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _elsewhere(t, name, device):
+    return ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                      f"{name} must be on CUDA device {device} like the other tensors, not on {t.get_device()}")
+
+
+def _on_gpu(t, name, dtype, device):
+    """The data pointer of a tensor on `device` (None stays None)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     return t.data_ptr()
 
 
-def _packed(t, name, dtype):
-    if t is not None and not t.is_contiguous():
+def _packed(t, name, dtype, device, shape=None):
+    """_on_gpu of a contiguous tensor, of `shape` where that is given."""
+    if t is None:
+        return None
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _on_gpu(t, name, dtype)
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _described(device, *descriptors):
+    """Refuses descriptors of tensors that are not on `device` (None: the caller built the descriptor)."""
+    for d in descriptors:
+        if d.device != device and d.device is not None:
+            raise ValueError(f"{type(d).__name__} of tensors on CUDA device {d.device}, not on {device} like the others")
 
 
 def kv_cache(k, v) -> KvCacheDesc:
@@ -410,9 +443,10 @@ def kv_cache(k, v) -> KvCacheDesc:
         raise ValueError("k and v must be 4-D tensors of one shape, dtype and layout")
     if k.stride(3) != 1:
         raise ValueError("the head dimension must have unit stride")
-    d = KvCacheDesc(_on_gpu(k, "k"), _on_gpu(v, "v"), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[2],
-                    k.shape[1], k.shape[3], _dtype_code(k))
-    d.tensors = (k, v)  # kept alive with the descriptor
+    device = _device_of(k, "k")
+    d = KvCacheDesc(_on_gpu(k, "k", None, device), _on_gpu(v, "v", None, device), k.shape[0], k.stride(0), k.stride(1),
+                    k.stride(2), k.shape[2], k.shape[1], k.shape[3], _dtype_code(k))
+    d.tensors, d.device = (k, v), device  # (the tensors live as long as the descriptor)
     return d
 
 
@@ -431,10 +465,11 @@ def kv_step(seq_lens, page_table, new_start=None, tokens=None, max_new=1) -> KvS
     if new_start is not None and new_start.numel() != batch + 1:
         raise ValueError("new_start must have batch + 1 elements")
     stride = page_table.stride(0) if batch > 1 else max(page_table.shape[1], 1)
-    d = KvStepDesc(_packed(seq_lens, "seq_lens", torch.int32), _packed(new_start, "new_start", torch.int32),
-                   _on_gpu(page_table, "page_table", torch.int32), stride, batch, tokens, max_new,
+    device = _device_of(seq_lens, "seq_lens")
+    d = KvStepDesc(_packed(seq_lens, "seq_lens", torch.int32, device), _packed(new_start, "new_start", torch.int32, device),
+                   _on_gpu(page_table, "page_table", torch.int32, device), stride, batch, tokens, max_new,
                    page_table.shape[1])
-    d.tensors = (seq_lens, new_start, page_table)
+    d.tensors, d.device = (seq_lens, new_start, page_table), device
     return d
 
 
@@ -446,50 +481,61 @@ def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e
     lengths = {w.numel() for w in (q_norm, k_norm) if w is not None}
     if len(lengths) > 1:
         raise ValueError("q_norm and k_norm must have one length")
-    d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32), max_pos, rot_dim, int(bool(interleaved)),
-                   _packed(q_norm, "q_norm", torch.float32), _packed(k_norm, "k_norm", torch.float32), eps)
-    d.tensors = (cos_sin, q_norm, k_norm)
+    device = next((_device_of(t, "a tensor of the rope") for t in (cos_sin, q_norm, k_norm) if t is not None), None)
+    d = KvRopeDesc(_packed(cos_sin, "cos_sin", torch.float32, device), max_pos, rot_dim, int(bool(interleaved)),
+                   _packed(q_norm, "q_norm", torch.float32, device), _packed(k_norm, "k_norm", torch.float32, device), eps)
+    d.tensors, d.device = (cos_sin, q_norm, k_norm), device
     if lengths:
         d.norm_dim = lengths.pop()
     return d
 
 
-def _token_rows(t, name, shape):
+def _token_rows(t, name, shape, device):
     """Pointer and token stride of rows [tokens, heads, head_dim] (heads adjacent within a token)."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     stride = t.stride()
     if stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be adjacent")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
     return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1] * shape[2])  # one token's stride is never used
 
 
-def _stream_of(t, stream):
-    """The raw handle of `stream`, or of the current stream of the CUDA tensor t's device."""
-    if stream is None:
+_torch_c = None  # torch's C module, once a call has imported torch
+
+
+def _stream_on(device, stream):
+    """The raw handle of `stream`, or of the current stream.  The library launches on the current device: `device`, where
+    the tensors are, has to be that one."""
+    global _torch_c
+    if _torch_c is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _stream(stream)
+        _torch_c = torch._C
+    if device < 0 or device != _torch_c._cuda_getDevice():
+        raise ValueError("the tensors must be on the current CUDA device, not on " +
+                         ("the host" if device < 0 else f"CUDA device {device}"))
+    return _torch_c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True):
     """Stores a step's k and v [tokens, kv_heads, head_dim] in the cache and writes q [tokens, q_heads, head_dim] to
     q_out (may be q; both None: no queries), q and k normed and rotated as `rope` says.  Rows may be strided parts
     of one projection's output."""
-    n, dim, dtype = step.tokens, cache.head_dim, k.dtype
+    n, dim, dtype, device = step.tokens, cache.head_dim, k.dtype, k.get_device()
+    if not cache.device == step.device == device:
+        _described(device, cache, step)
     shape = (n, cache.kv_heads, dim)
-    kp, ks = _token_rows(k, "k", shape)
-    vp, vs = _token_rows(v, "v", shape)
+    kp, ks = _token_rows(k, "k", shape, device)
+    vp, vs = _token_rows(v, "v", shape, device)
     qp = op = None
     qs = os_ = heads = 0
     if q is not None:
         shape = q.shape
         heads = shape[1]
-        qp, qs = _token_rows(q, "q", (n, heads, dim))
+        qp, qs = _token_rows(q, "q", (n, heads, dim), device)
         if q_out is not None:
-            op, os_ = _token_rows(q_out, "q_out", shape)
+            op, os_ = _token_rows(q_out, "q_out", shape, device)
             if q_out.dtype != dtype:
                 raise TypeError("q_out must have q's dtype")
         if q.dtype != dtype:
@@ -498,10 +544,13 @@ def kv_append(cache, step, q, k, v, q_out, rope=None, stream=None, *, check=True
         raise ValueError("q_out needs q")
     if v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    if rope is not None and rope.norm_dim not in (None, dim):
-        raise ValueError(f"q_norm and k_norm must have head_dim = {dim} elements, not {rope.norm_dim}")
+    if rope is not None:
+        if rope.device != device:
+            _described(device, rope)
+        if rope.norm_dim != dim and rope.norm_dim is not None:
+            raise ValueError(f"q_norm and k_norm must have head_dim = {dim} elements, not {rope.norm_dim}")
     st = load_library().kv_append(_address(cache), _address(step), None if rope is None else _address(rope), qp, qs, heads,
-                                  kp, ks, vp, vs, _dtype_code(k), op, os_, _stream_of(k, stream))
+                                  kp, ks, vp, vs, _dtype_code(k), op, os_, _stream_on(device, stream))
     if check:
         _check(st, "kv_append")
     return st
@@ -517,16 +566,18 @@ def kv_attention_workspace_size(q_heads, kv_heads, head_dim, max_new=1) -> int:
 def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, lse=None, stream=None, check=True):
     """Attention of the step's new tokens q [tokens, q_heads, head_dim] over the cache into out (same shape and
     dtype); scale defaults to head_dim ** -0.5, lse (f32 [tokens, q_heads]) is optional."""
-    n, dim, shape = step.tokens, cache.head_dim, q.shape
+    n, dim, shape, device = step.tokens, cache.head_dim, q.shape, q.get_device()
+    if not cache.device == step.device == device:
+        _described(device, cache, step)
     heads = shape[1]
-    qp, qs = _token_rows(q, "q", (n, heads, dim))
-    op, os_ = _token_rows(out, "out", shape)
+    qp, qs = _token_rows(q, "q", (n, heads, dim), device)
+    op, os_ = _token_rows(out, "out", shape, device)
     if out.dtype != q.dtype:
         raise TypeError("out must have q's dtype")
     lp = None
     if lse is not None:
         import torch
-        lp = _packed(lse, "lse", torch.float32)
+        lp = _packed(lse, "lse", torch.float32, device)
         if lse.numel() != n * heads:
             raise ValueError("lse must be [tokens, q_heads]")
     if workspace is None:
@@ -537,7 +588,7 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
             workspace.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
     st = load_library().kv_attention(_address(cache), _address(step), qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
-                                     _packed(workspace, "workspace", None), workspace.nbytes, _stream_of(q, stream))
+                                     _packed(workspace, "workspace", None, device), workspace.nbytes, _stream_on(device, stream))
     if check:
         _check(st, "kv_attention")
     return st
@@ -549,29 +600,26 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
     (standing drafts, the drawn token, -1s) and accepted int32 [batch]."""
     import torch
     batch, rows, vocab = target.shape
-    n, f32, i32 = rows - 1, torch.float32, torch.int32
+    n, f32, i32, device = rows - 1, torch.float32, torch.int32, target.get_device()
     if draft is not None and draft.shape != (batch, n, vocab):
         raise ValueError("draft must be [batch, n, vocab]")
     if n == 0:
         draft = None  # nothing was drafted
+
     def rows_of(t, name, count):  # pointer and strides (those of an extent of one are never used)
         s0, s1, s2 = t.stride()
         if s2 != 1 and vocab > 1:
             raise ValueError(f"{name} must have unit stride along the vocabulary")
-        return _on_gpu(t, name, f32), (s0 if batch > 1 else count * vocab), (s1 if count > 1 else vocab)
-
-    def whole(t, name, shape, dtype):
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
-        return _packed(t, name, dtype)
+        return _on_gpu(t, name, f32, device), (s0 if batch > 1 else count * vocab), (s1 if count > 1 else vocab)
 
     tp, ts, tr = rows_of(target, "target", rows)
     dp, ds, dr = (None, 0, 0) if draft is None else rows_of(draft, "draft", n)
-    st = load_library().draft_verify(tp, ts, tr, dp, ds, dr, whole(draft_tokens, "draft_tokens", (batch, n), i32),
-                                     None if n_drafts is None else whole(n_drafts, "n_drafts", (batch,), i32),
-                                     whole(uniforms, "uniforms", (batch, rows), f32), batch, n, vocab,
-                                     whole(tokens, "tokens", (batch, rows), i32), whole(accepted, "accepted", (batch,), i32),
-                                     _stream_of(target, stream))
+    out = (batch, rows)
+    st = load_library().draft_verify(tp, ts, tr, dp, ds, dr, _packed(draft_tokens, "draft_tokens", i32, device, (batch, n)),
+                                     _packed(n_drafts, "n_drafts", i32, device, (batch,)),
+                                     _packed(uniforms, "uniforms", f32, device, out), batch, n, vocab,
+                                     _packed(tokens, "tokens", i32, device, out),
+                                     _packed(accepted, "accepted", i32, device, (batch,)), _stream_on(device, stream))
     if check:
         _check(st, "draft_verify")
     return st

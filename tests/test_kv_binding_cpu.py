@@ -58,7 +58,7 @@ class Library:
 def lib(monkeypatch):
     library = Library()
     monkeypatch.setattr(_binding, "load_library", lambda path=None: library)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
     return library
 
@@ -135,3 +135,55 @@ def test_norms_have_one_weight_per_element_of_a_head(lib):
         with pytest.raises(ValueError):
             append(rope=mnb.kv_rope(**bad))
     assert len(lib.calls) == 3
+
+
+def verify(device=0, **kw):
+    t = dict(target=f32(2, 4, 50, device=device), draft=f32(2, 3, 50, device=device), draft_tokens=i32(2, 3, device=device),
+             uniforms=f32(2, 4, device=device), tokens=i32(2, 4, device=device), accepted=i32(2, device=device),
+             n_drafts=i32(2, device=device))
+    t.update(kw)
+    return mnb.draft_verify(t["target"], t["draft"], t["draft_tokens"], t["uniforms"], t["tokens"], t["accepted"],
+                            n_drafts=t["n_drafts"])
+
+
+@pytest.mark.parametrize("where", [1, -1])  # another GPU, the host
+def test_every_tensor_is_on_the_current_device(lib, monkeypatch, where):
+    """The library launches on the current device, whatever device the tensors are on."""
+    far = rows(2, device=where)
+    for bad in (dict(q=rows(4, device=where)), dict(k=far), dict(v=far), dict(out=rows(4, device=where))):
+        with pytest.raises(ValueError):
+            append(**bad)
+    for bad in (dict(q=rows(4, device=where)), dict(out=rows(4, device=where)), dict(ws=Tensor((1 << 20,), torch.uint8, where)),
+                dict(lse=f32(3, 4, device=where))):
+        with pytest.raises(ValueError):
+            attend(**bad)
+    for name in ("draft_tokens", "tokens"):
+        with pytest.raises(ValueError):
+            verify(**{name: i32(2, 3 if name == "draft_tokens" else 4, device=where)})
+    for bad in (dict(target=f32(2, 4, 50, device=where)), dict(draft=f32(2, 3, 50, device=where)),
+                dict(uniforms=f32(2, 4, device=where)), dict(accepted=i32(2, device=where)), dict(n_drafts=i32(2, device=where))):
+        with pytest.raises(ValueError):
+            verify(**bad)
+    # descriptors: tensors of one device, which is the current one at the call
+    for make in (lambda: mnb.kv_cache(Tensor((9, 2, 16, 64)), Tensor((9, 2, 16, 64), device=where)),
+                 lambda: mnb.kv_step(i32(3), i32(3, 4, device=where)), lambda: mnb.kv_step(i32(3, device=where), i32(3, 4)),
+                 lambda: mnb.kv_step(i32(3), i32(3, 4), new_start=i32(4, device=where), tokens=3),
+                 lambda: mnb.kv_rope(f32(100, 64), q_norm=f32(64, device=where)),
+                 lambda: mnb.kv_rope(f32(100, 64, device=where), k_norm=f32(64))):
+        with pytest.raises(ValueError):
+            make()
+    if where > 0:
+        for bad in (dict(c=cache(where)), dict(s=step(where)), dict(rope=mnb.kv_rope(q_norm=f32(64, device=where)))):
+            with pytest.raises(ValueError):
+                append(**bad)
+        for bad in (dict(c=cache(where)), dict(s=step(where))):
+            with pytest.raises(ValueError):
+                attend(**bad)
+    assert lib.calls == []
+    if where > 0:  # and with that device current, all of them run, on its stream
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: where, raising=False)
+        append(cache(where), step(where), mnb.kv_rope(q_norm=f32(64, device=where)), rows(4, where), rows(2, where),
+               rows(2, where), rows(4, where))
+        attend(cache(where), step(where), rows(4, where), rows(4, where), Tensor((1 << 20,), torch.uint8, where))
+        verify(where)
+        assert [args[-1] for _, args in lib.calls] == [1000 + where] * 3
