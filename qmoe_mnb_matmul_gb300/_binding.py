@@ -4,9 +4,10 @@ library's CUDA kernels.  There is no fallback: if the library has not been
 built, loading it raises.
 
 Tensors are torch tensors on the current CUDA device (contiguous); raw device
-pointers may be passed as ints instead (the paged-cache and draft calls take
-tensors, with strides where their text says so, and refuse those of another device).  ``stream`` is a torch.cuda.Stream, a
-raw cudaStream_t handle (int), or None for torch's current stream.
+pointers may be passed as ints instead.  The paged-cache and draft calls take
+tensors only, with strides where their text says so.  ``stream`` is a
+torch.cuda.Stream, a raw cudaStream_t handle (int), or None for torch's current
+stream.
 """
 from __future__ import annotations
 
@@ -168,6 +169,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _stream_for(t, stream):
+    """_stream for a call on the tensor t: the library launches on the current device, so t may not be on another GPU."""
+    import torch
+    device = torch.cuda.current_device()
+    if not isinstance(t, int) and t.get_device() not in (device, -1):
+        raise ValueError(f"the tensors are on CUDA device {t.get_device()}, the current device is {device}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def _check(status: int, call: str):
     if status != 0:
         raise MnbError(status, call)
@@ -204,7 +214,7 @@ def mnb_matmul(A, B_packed, scales, zero_points, N, bits, block_size, Y, workspa
     ws_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel() * workspace.element_size()
     st = load_library().mnb_matmul(_ptr(A), a_dtype, M, K, _ptr(B_packed), _ptr(scales), scale_dtype,
                                    _ptr(zero_points), N, bits, block_size, _ptr(Y), y_dtype, _ptr(workspace),
-                                   ws_bytes, _stream(stream))
+                                   ws_bytes, _stream_for(A, stream))
     if check:
         _check(st, "mnb_matmul")
     return st
@@ -221,7 +231,7 @@ def mnb_matmul_int8a(A, B_packed, scales, zero_points, N, bits, block_size, Y, s
     scale_dtype = _dtype_code(scales) if scale_dtype is None else scale_dtype
     y_dtype = _dtype_code(Y) if y_dtype is None else y_dtype
     st = load_library().mnb_matmul_int8a(_ptr(A), a_dtype, M, K, _ptr(B_packed), _ptr(scales), scale_dtype,
-                                         _ptr(zero_points), N, bits, block_size, _ptr(Y), y_dtype, _stream(stream))
+                                         _ptr(zero_points), N, bits, block_size, _ptr(Y), y_dtype, _stream_for(A, stream))
     if check:
         _check(st, "mnb_matmul_int8a")
     return st
@@ -240,7 +250,7 @@ def mnb_gate_up_swiglu(A, B_packed, scales, zero_points, I, bits, block_size, Y,
     y_dtype = _dtype_code(Y) if y_dtype is None else y_dtype
     st = load_library().mnb_gate_up_swiglu(_ptr(A), a_dtype, M, K, _ptr(B_packed), _ptr(scales), scale_dtype,
                                            _ptr(zero_points), I, bits, block_size, layout, _ptr(Y), y_dtype,
-                                           _stream(stream))
+                                           _stream_for(A, stream))
     if check:
         _check(st, "mnb_gate_up_swiglu")
     return st
@@ -263,7 +273,7 @@ def mnb_prepack(B_packed, scales, zero_points, N, K, bits, block_size, dst, iden
     desc = PrepackedDesc()
     st = load_library().mnb_prepack(_ptr(B_packed), _ptr(scales), scale_dtype, _ptr(zero_points), N, K, bits,
                                     block_size, ctypes.c_uint64(identity), _ptr(dst), dst_bytes, ctypes.byref(desc),
-                                    _stream(stream))
+                                    _stream_for(B_packed, stream))
     if not check:
         return st, desc
     _check(st, "mnb_prepack")
@@ -280,7 +290,7 @@ def mnb_matmul_prepacked(A, desc, prepacked, Y, stream=None, *, K=None, M=None, 
     a_dtype = _dtype_code(A) if a_dtype is None else a_dtype
     y_dtype = _dtype_code(Y) if y_dtype is None else y_dtype
     st = load_library().mnb_matmul_prepacked(_ptr(A), a_dtype, M, K, ctypes.byref(desc), _ptr(prepacked), _ptr(Y),
-                                             y_dtype, _stream(stream))
+                                             y_dtype, _stream_for(A, stream))
     if check:
         _check(st, "mnb_matmul_prepacked")
     return st
@@ -309,7 +319,7 @@ def qmoe_forward(X, router_logits, k, normalize_topk, fc1_w, fc1_scales, fc1_zp,
     st = load_library().qmoe_forward(_ptr(X), act_dtype, T, H, _ptr(router_logits), E, k, int(bool(normalize_topk)),
                                      _ptr(fc1_w), _ptr(fc1_scales), _ptr(fc1_zp), fc1_bits, _ptr(fc2_w),
                                      _ptr(fc2_scales), _ptr(fc2_zp), fc2_bits, I, block_size, fc1_layout, _ptr(Y),
-                                     _ptr(workspace), workspace_bytes, _stream(stream))
+                                     _ptr(workspace), workspace_bytes, _stream_for(X, stream))
     if check:
         _check(st, "qmoe_forward")
     return st
@@ -341,7 +351,7 @@ def qmoe_forward_ex(X, router_logits, k, normalize_topk, fc1_w, fc1_scales, fc1_
     st = load_library().qmoe_forward_ex(_ptr(X), act_dtype, T, H, _ptr(router_logits), E, k, int(bool(normalize_topk)),
                                         _ptr(fc1_w), _ptr(fc1_scales), _ptr(fc1_zp), fc1_bits, _ptr(fc2_w),
                                         _ptr(fc2_scales), _ptr(fc2_zp), fc2_bits, I, block_size, fc1_layout, _ptr(Y),
-                                        _ptr(workspace), workspace_bytes, ctypes.byref(opts), _stream(stream))
+                                        _ptr(workspace), workspace_bytes, ctypes.byref(opts), _stream_for(X, stream))
     if check:
         _check(st, "qmoe_forward_ex")
     return st
@@ -361,7 +371,7 @@ def qmoe_forward_static(X, router_logits, k, normalize_topk, fc1_w, fc1_scales, 
     st = load_library().qmoe_forward_static(_ptr(X), act_dtype, T, H, _ptr(router_logits), E, k,
                                             int(bool(normalize_topk)), _ptr(fc1_w), _ptr(fc1_scales), _ptr(fc1_zp),
                                             fc1_bits, _ptr(fc2_w), _ptr(fc2_scales), _ptr(fc2_zp), fc2_bits, I,
-                                            block_size, fc1_layout, _ptr(Y), _stream(stream))
+                                            block_size, fc1_layout, _ptr(Y), _stream_for(X, stream))
     if check:
         _check(st, "qmoe_forward_static")
     return st
@@ -373,7 +383,7 @@ def qmoe_route(logits, k, normalize_topk, topk_idx, topk_w, stream=None, *, T=No
     if T is None:
         T = logits.numel() // E
     st = load_library().qmoe_route(_ptr(logits), T, E, k, int(bool(normalize_topk)), _ptr(topk_idx), _ptr(topk_w),
-                                   _stream(stream))
+                                   _stream_for(logits, stream))
     if check:
         _check(st, "qmoe_route")
     return st
@@ -385,7 +395,7 @@ def qmoe_permute(topk_idx, E, counts, offsets, perm, stream=None, *, T=None, k=N
     if T is None:
         T = topk_idx.numel() // k
     st = load_library().qmoe_permute(_ptr(topk_idx), T, k, E, _ptr(counts), _ptr(offsets), _ptr(perm),
-                                     _stream(stream))
+                                     _stream_for(topk_idx, stream))
     if check:
         _check(st, "qmoe_permute")
     return st
@@ -626,14 +636,14 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
 
 
 def mnb_unpack_codes(B_packed, rows, K, bits, block_size, codes, stream=None, *, check=True):
-    st = load_library().mnb_unpack_codes(_ptr(B_packed), rows, K, bits, block_size, _ptr(codes), _stream(stream))
+    st = load_library().mnb_unpack_codes(_ptr(B_packed), rows, K, bits, block_size, _ptr(codes), _stream_for(B_packed, stream))
     if check:
         _check(st, "mnb_unpack_codes")
     return st
 
 
 def mnb_pack_codes(codes, rows, K, bits, block_size, B_packed, stream=None, *, check=True):
-    st = load_library().mnb_pack_codes(_ptr(codes), rows, K, bits, block_size, _ptr(B_packed), _stream(stream))
+    st = load_library().mnb_pack_codes(_ptr(codes), rows, K, bits, block_size, _ptr(B_packed), _stream_for(codes, stream))
     if check:
         _check(st, "mnb_pack_codes")
     return st
@@ -652,7 +662,7 @@ def mnb_quantize_int3(W, block_size, scale_dtype, B_packed=None, scales=None, st
     if scales is None:
         scales = torch.empty((N, nb), dtype=sdt, device=W.device)
     st = load_library().mnb_quantize_int3(_ptr(W), _dtype_code(W), N, K, block_size, _ptr(B_packed), _ptr(scales),
-                                          scale_dtype, _stream(stream))
+                                          scale_dtype, _stream_for(W, stream))
     if check:
         _check(st, "mnb_quantize_int3")
     return B_packed, scales

@@ -38,6 +38,9 @@ class Tensor:
     def data_ptr(self):
         return 0x10000
 
+    def element_size(self):
+        return self.dtype.itemsize
+
     @property
     def nbytes(self):
         return self.numel() * self.dtype.itemsize
@@ -187,3 +190,38 @@ def test_every_tensor_is_on_the_current_device(lib, monkeypatch, where):
         attend(cache(where), step(where), rows(4, where), rows(4, where), Tensor((1 << 20,), torch.uint8, where))
         verify(where)
         assert [args[-1] for _, args in lib.calls] == [1000 + where] * 3
+
+
+def products(where):
+    """Every other call of the binding that launches, with its first tensor on device `where`."""
+    u8 = lambda *shape: Tensor(shape, torch.uint8)  # noqa: E731
+    A, W, s, Y = f32(1, 64, device=where), u8(32, 2, 16), f32(32, 2), f32(1, 32)
+    qm = (f32(1, 8), 2, True, u8(8, 64, 32), f32(8, 64, 2), None, 4, u8(8, 64, 16), f32(8, 64, 1), None, 4, 32, 32, f32(1, 64))
+    Wd = Tensor((32, 2, 16), torch.uint8, where)
+    yield lambda: mnb.mnb_matmul(A, W, s, None, 32, 4, 32, Y, workspace=u8(64))
+    yield lambda: mnb.mnb_matmul_int8a(A, W, s, None, 32, 4, 32, Y)
+    yield lambda: mnb.mnb_gate_up_swiglu(A, W, s, None, 16, 4, 32, Y)
+    yield lambda: mnb.mnb_prepack(Wd, s, None, 32, 64, 4, 32, u8(4096))
+    yield lambda: mnb.mnb_matmul_prepacked(A, mnb.PrepackedDesc(), u8(4096), Y)
+    yield lambda: mnb.qmoe_forward(A, *qm, u8(1 << 20))
+    yield lambda: mnb.qmoe_forward_ex(A, *qm, u8(1 << 20))
+    yield lambda: mnb.qmoe_forward_static(A, *qm)
+    yield lambda: mnb.qmoe_route(f32(1, 8, device=where), 2, True, i32(1, 2), f32(1, 2))
+    yield lambda: mnb.qmoe_permute(i32(1, 2, device=where), 8, i32(8), i32(9), i32(2))
+    yield lambda: mnb.mnb_unpack_codes(Wd, 32, 64, 4, 32, u8(32, 64))
+    yield lambda: mnb.mnb_pack_codes(Tensor((32, 64), torch.uint8, where), 32, 64, 4, 32, u8(32, 2, 16))
+    yield lambda: mnb.mnb_quantize_int3(A, 32, mnb.F32, u8(1, 2, 12), f32(1, 2))
+
+
+def test_the_other_calls_do_not_launch_for_tensors_of_another_device(lib, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    calls = list(products(1))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    assert lib.calls == []
+    for call in products(0):
+        call()
+    assert len(lib.calls) == len(calls)
+    mnb.qmoe_route(0x10000, 2, True, 0x20000, 0x30000, T=1, E=8)  # raw pointers are the caller's
+    assert len(lib.calls) == len(calls) + 1
