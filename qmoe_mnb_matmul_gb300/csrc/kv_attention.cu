@@ -36,7 +36,6 @@ constexpr int kFewParts = 16;
 constexpr int kJoinGridY = 16;  // CTAs of a pair
 
 // Writes columns d, d + 1 of a row (lane's share of it) and the row's log-sum-exp.
-template <int DP>
 __device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, int flat, int head_kv, int d, float2 s,
                                            float m, float l) {
     const int tok = a.by_group(flat), head = head_kv * a.group + flat - tok * a.group;
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
                 }
             }
 #pragma unroll
-            for (int v = 0; v < NV; ++v) join_store<DP>(a, out_dtype, j.z + row, head_kv, (v * 32 + lane) * 2, acc[v], m, l);
+            for (int v = 0; v < NV; ++v) join_store(a, out_dtype, j.z + row, head_kv, (v * 32 + lane) * 2, acc[v], m, l);
         }
         return;
     }
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
                 s.x += sums[x][threadIdx.x].x;
                 s.y += sums[x][threadIdx.x].y;
             }
-            join_store<DP>(a, out_dtype, j.z + row, head_kv, threadIdx.x * 2, s, m, l);
+            join_store(a, out_dtype, j.z + row, head_kv, threadIdx.x * 2, s, m, l);
         }
         __syncthreads();
     }
