@@ -410,11 +410,12 @@ typedef struct {
  * (f32 or the cache's), each with its own stride in elements between tokens,
  * so that they may be parts of one projection's output rows; q_out like q, and
  * may be q itself.  q and q_out may both be NULL.  Computed in fp32, rounded
- * once to the cache's dtype (q_out: to dtype).  A token whose position has no
- * page (a page number outside [0, num_pages), a position past max_pages *
- * page_size) or no row of cos_sin is skipped, with its q_out row, and records
- * MNB_ERR_CONTENT in the device error word.  Pointers and strides in whole
- * 16-byte units (strides: multiples of 8 elements). */
+ * once to the cache's dtype (q_out: to dtype; what an fp16 cache cannot hold
+ * becomes an infinity there).  A token whose position has no page (a page number
+ * outside [0, num_pages), a position past max_pages * page_size) or no row of
+ * cos_sin is skipped, with its q_out row, and records MNB_ERR_CONTENT in the
+ * device error word.  Pointers and strides in whole 16-byte units (strides:
+ * multiples of 8 elements). */
 mnb_status kv_append(const kv_cache_desc* cache, const kv_step_desc* step, const kv_rope_desc* rope, const void* q,
                      int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, mnb_dtype dtype, void* q_out, int64_t q_out_stride, mnb_stream_t stream);

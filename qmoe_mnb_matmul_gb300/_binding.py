@@ -231,7 +231,8 @@ def mnb_matmul_int8a(A, B_packed, scales, zero_points, N, bits, block_size, Y, s
     scale_dtype = _dtype_code(scales) if scale_dtype is None else scale_dtype
     y_dtype = _dtype_code(Y) if y_dtype is None else y_dtype
     st = load_library().mnb_matmul_int8a(_ptr(A), a_dtype, M, K, _ptr(B_packed), _ptr(scales), scale_dtype,
-                                         _ptr(zero_points), N, bits, block_size, _ptr(Y), y_dtype, _stream_for(A, stream))
+                                         _ptr(zero_points), N, bits, block_size, _ptr(Y), y_dtype,
+                                         _stream_for(A, stream))
     if check:
         _check(st, "mnb_matmul_int8a")
     return st
@@ -598,7 +599,8 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
             workspace.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
     st = load_library().kv_attention(_address(cache), _address(step), qp, qs, heads, _dtype_code(q), op, os_,
                                      lp, dim ** -0.5 if scale is None else scale, window,
-                                     _packed(workspace, "workspace", None, device), workspace.nbytes, _stream_on(device, stream))
+                                     _packed(workspace, "workspace", None, device), workspace.nbytes,
+                                     _stream_on(device, stream))
     if check:
         _check(st, "kv_attention")
     return st
@@ -625,7 +627,8 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
     tp, ts, tr = rows_of(target, "target", rows)
     dp, ds, dr = (None, 0, 0) if draft is None else rows_of(draft, "draft", n)
     out = (batch, rows)
-    st = load_library().draft_verify(tp, ts, tr, dp, ds, dr, _packed(draft_tokens, "draft_tokens", i32, device, (batch, n)),
+    st = load_library().draft_verify(tp, ts, tr, dp, ds, dr,
+                                     _packed(draft_tokens, "draft_tokens", i32, device, (batch, n)),
                                      _packed(n_drafts, "n_drafts", i32, device, (batch,)),
                                      _packed(uniforms, "uniforms", f32, device, out), batch, n, vocab,
                                      _packed(tokens, "tokens", i32, device, out),
@@ -636,7 +639,8 @@ def draft_verify(target, draft, draft_tokens, uniforms, tokens, accepted, *, n_d
 
 
 def mnb_unpack_codes(B_packed, rows, K, bits, block_size, codes, stream=None, *, check=True):
-    st = load_library().mnb_unpack_codes(_ptr(B_packed), rows, K, bits, block_size, _ptr(codes), _stream_for(B_packed, stream))
+    st = load_library().mnb_unpack_codes(_ptr(B_packed), rows, K, bits, block_size, _ptr(codes),
+                                         _stream_for(B_packed, stream))
     if check:
         _check(st, "mnb_unpack_codes")
     return st

@@ -13,9 +13,9 @@
 // and its partner run, so that a rotation needs no exchange between lanes.  A
 // warp takes one token (or a share of its heads, where tokens are few): its
 // angles, times the norm's weights, stay in registers over the heads, and those
-// are read two steps at a time (four
-// spilled registers at four CTAs per SM and took 75 us instead of 56 for 16920
-// tokens of 32 heads).
+// are read two steps at a time (at four CTAs per SM and 64 registers that spills up
+// to 36 bytes; four steps spilled more and took 75 us instead of 56 for 16920 tokens
+// of 32 heads).
 //
 // Measured: one token of 16 + 8 + 8 heads of 128 in fp32 2.5 us; prompts of 16920 tokens
 // in bf16 55.6 us, 5.1 TB/s (286 MB), between instruction issue (57 %) and load latency

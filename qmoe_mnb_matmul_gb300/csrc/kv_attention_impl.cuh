@@ -51,12 +51,16 @@
 //
 // Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens,
 // 16 query heads over 8, 1.09 GB: 173 us, 6.3 TB/s; one sequence of 131072 tokens, 32
-// over 4, 268 MB: 50 us; 777 tokens: 7.1 us, all latency (finding the range 1.5, the
+// over 4, 268 MB: 51 us; 777 tokens: 7.2 us, all latency (finding the range 1.5, the
 // first tile 2.5, the join 2).  16 sequences with 1 .. 5 drafts, 24 .. 40 rows, 294 MB:
-// 82 us in fp16 (79 without the second part's own sum), bound by the latency of the matrix instructions (two compute warps per
-// scheduler, tensor pipe 33 % busy).  What was slower: rows on the instructions' long
-// side (187 us for the batch), one producer warp for keys and values (219), a page
-// lookup that a tile waits for (344).
+// 82 us in fp16 (79 without the second part's own sum), 80 in bf16, bound by the latency
+// of the matrix instructions (two compute warps per scheduler, tensor pipe 31 % busy).
+// Everything lives in registers there, and two CTAs per SM leave 168 of them: the 8-row
+// kernels spill nothing, those of 32 and 64 rows at a width of 128 spill 184 .. 268 bytes
+// (fp32 queries over an fp16 cache, 64 rows: 788).  What was slower: rows on the
+// instructions' long side (187 us for the batch), one producer warp for keys and values
+// (219), a page lookup that a tile waits for (344), the second parts' sum carried on into
+// the first parts' (86 us for the drafts).
 #pragma once
 
 #include <cuda.h>
@@ -559,7 +563,10 @@ __device__ __forceinline__ Place merge_place(int rg, int g, int half, int k) {
 // with columns that are not finite (bits of `odd`: share 8 * (2 g + half) + step), each
 // of them is looked through once more and gets the sum of its values that are not
 // finite (if there are none, fp32 did not hold the sum, and it stays).  Looking at each
-// stored result costs 0.1 us of a short call (7.1 us of 777 tokens).
+// stored result costs 0.1 us of a short call (777 tokens: 7.2 us); a cache that does hold
+// infinities is slower (7.3 ms for 64 sequences of up to 8192 tokens with one whole row of
+// them each).  Loads of eight tokens at a time made that 2.9 ms, and every other call 0.5 %
+// slower by the size of the code.
 template <int DT, bool QF32, int DP, int ROWS>
 __device__ __forceinline__ void odd_columns(const KvAttnArgs& a, const Smem& sm, const Walk& w, int nt, bool whole,
                                             int part, int rg, uint32_t odd) {
