@@ -385,6 +385,54 @@ typedef struct {
     int32_t batch, tokens, max_new, max_pages;
 } kv_step_desc;
 
+/* The pages of a pool and who holds them (device arrays of the caller, kept
+ * over the steps).
+ *   held         [batch]: pages of each sequence, the first held[b] entries of
+ *                its page_table row.
+ *   page_table   [batch, max_pages], rows table_stride apart; in and out.
+ *   free_pages   [num_pages], in and out: a stack, of which the first
+ *                free_count[0] entries are the free pages, the last on top.
+ *   held_out [batch], free_count_out [1]: the same after the step; they may be
+ *                held and free_count themselves.
+ * page_size is the tokens of a page. */
+typedef struct {
+    const int32_t* held;
+    int32_t* page_table;
+    int64_t table_stride;
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* held_out;
+    int32_t* free_count_out;
+    int32_t batch, max_pages, num_pages, page_size;
+} kv_pool_desc;
+
+/* Plans a step on the device: sequence b keeps its first keep[b] tokens in the
+ * cache (the others, fallen drafts or a finished sequence's, are dropped) and
+ * gets add[b] new ones.  Both [batch]; keep[b] <= held[b] * page_size.
+ *   seq_lens  [batch] out: keep[b] + the new tokens: kv_step_desc's.
+ *   new_start [batch + 1] out: kv_step_desc's.
+ *   slots     [max_tokens] out or NULL: for each new token its page *
+ *             page_size + row in the page.  Entries behind the last new token
+ *             are left alone.
+ *   refused   [batch] out or NULL: 1 where a sequence's new tokens were refused.
+ * With need = ceil((keep + add) / page_size) a sequence gives its last held -
+ * need pages back or takes need - held.  What is given back lies on the stack
+ * before anything is taken, the first sequence's first page on top; the first
+ * sequence takes first, from the top, so that a step that adds tokens and one
+ * that drops the same tokens undo each other.  A sequence's new tokens are refused (none
+ * are added; its kept tokens and its pages stay) where it needs more than
+ * max_pages pages or 2^31 - 4097 tokens; else where it takes pages and the pages
+ * asked for up to and with it are more than there are; or where the tokens asked
+ * for up to and with it are more than max_tokens.  (What these sums count does
+ * not depend on refusals, but for the first reason.)
+ * The outputs of batch entries may be its inputs (seq_lens may be keep), every
+ * other overlap is not allowed.  An entry outside its range (a negative count,
+ * keep past the pages held) is cut to it, a page number outside [0, num_pages)
+ * gives the slot -1; both record MNB_ERR_CONTENT.  batch <= 8192, else
+ * MNB_ERR_UNSUPPORTED; max_tokens <= 2^30. */
+mnb_status kv_plan(const kv_pool_desc* pool, const int32_t* keep, const int32_t* add, int32_t* seq_lens,
+                   int32_t* new_start, int64_t max_tokens, int64_t* slots, int32_t* refused, mnb_stream_t stream);
+
 /* What happens to queries and keys before they are used.
  *   q_norm, k_norm  [head_dim] fp32 or NULL: per-head norm x / sqrt(mean(x^2)
  *                   + eps) * weight, first.
@@ -455,6 +503,62 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
 mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, const void* q, int64_t q_stride,
                         int64_t q_heads, mnb_dtype dtype, void* out, int64_t out_stride, float* lse, float scale,
                         int64_t window, void* workspace, size_t workspace_bytes, mnb_stream_t stream);
+
+/* What changes a step's logits for each sequence (device arrays of the caller,
+ * kept over the steps; any of them may be NULL).
+ *   temperature  [batch] fp32 (NULL: 1).  0 or less: the largest value wins.
+ *   history      [batch, history_columns], rows history_stride apart: the tokens
+ *                so far, history_lens[b] of them, the first prompt_lens[b] (NULL:
+ *                none) the prompt's.  Numbers outside the vocabulary count for
+ *                nothing.
+ *   repetition (NULL: 1), frequency, presence (NULL: 0)  [batch] fp32.
+ *   bias_tokens, bias_values  [batch, biases], rows bias_stride apart: of several
+ *                biases of one token the last one counts, numbers outside the
+ *                vocabulary (padding) for nothing. */
+typedef struct {
+    const float* temperature;
+    const int32_t* history;
+    int64_t history_stride;
+    const int32_t* history_lens;
+    const int32_t* prompt_lens;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_tokens;
+    const float* bias_values;
+    int64_t bias_stride;
+    int32_t batch, history_columns, biases;
+} token_rules;
+
+/* The probabilities (or the changed logits) of a step's rows, ready for
+ * draft_verify.  Row i of sequence b follows the drafts draft_tokens[b, 0 .. i -
+ * 1].  With n the number of times that token v occurs in the generated part of
+ * the history and those drafts, in fp32, one rounding each:
+ *   x = logit;  where v occurs in the history or the drafts: x = x > 0 ?
+ *   x / repetition : x * repetition;  x = x - frequency * n;  where n > 0:
+ *   x = x - presence;  x = x + bias;  where the mask forbids v: x = -infinity.
+ * softmax != 0: out = e^((x - m) / T) / sum e^((x - m) / T), m the largest x; with
+ * T <= 0 (or NaN) 1 for the first of the largest x and 0 for the others.  A row
+ * with nothing left (every x = -infinity) gets zeros; a NaN that the mask does
+ * not forbid, and with T > 0 an infinity, makes the whole row NaN.  softmax ==
+ * 0: out = x / T (T <= 0: x).
+ *   logits   f32, f16 or bf16: [batch, rows, vocab] with strides in elements
+ *            between sequences and rows, or with row_start [batch + 1] a ragged
+ *            step's [tokens, vocab] rows: row i of sequence b is row row_start[b] + i,
+ *            those with row_start[b] + i < row_start[b + 1] exist, and the others
+ *            of out are left alone.
+ *   draft_tokens [batch, rows - 1] or NULL.
+ *   mask     or NULL: bit v % 32 of word v / 32 of a row's ceil(vocab / 32) words
+ *            is 1 where v is allowed; strides in words (0 shares a row).
+ *   out      fp32 [batch, rows, vocab] with strides; may be fp32 logits of the
+ *            same strides (without row_start), else no overlap.
+ * vocab < 2^22, and no more than 921600 with a history or drafts or with biases,
+ * 460800 with both; rows <= 1025; else MNB_ERR_UNSUPPORTED. */
+mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_stride, int64_t logits_row_stride,
+                       const int32_t* row_start, int64_t tokens, const token_rules* rules,
+                       const int32_t* draft_tokens, const uint32_t* mask, int64_t mask_seq_stride,
+                       int64_t mask_row_stride, int64_t rows, int64_t vocab, float* out, int64_t out_seq_stride,
+                       int64_t out_row_stride, int softmax, mnb_stream_t stream);
 
 /* Verification of drafted tokens against the target's probabilities, from
  * given uniform numbers in [0, 1).  Sequence b has n = n_drafts[b] drafts (NULL:

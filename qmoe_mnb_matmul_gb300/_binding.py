@@ -61,6 +61,25 @@ class KvRopeDesc(ctypes.Structure):
     norm_dim = None  # length of the norms' weights, where kv_rope saw them
 
 
+class KvPoolDesc(ctypes.Structure):
+    """kv_pool_desc: the pages of a pool (see kv_pool)."""
+    _fields_ = [("held", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("held_out", ctypes.c_void_p),
+                ("free_count_out", ctypes.c_void_p), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+    device = None
+
+
+class TokenRules(ctypes.Structure):
+    """token_rules: penalties, biases and temperatures of a batch (see token_rules)."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64),
+                ("history_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("bias_stride", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("history_columns", ctypes.c_int32), ("biases", ctypes.c_int32)]
+    device = None
+
+
 class MnbError(RuntimeError):
     def __init__(self, status: int, call: str):
         super().__init__(f"{call} failed: {STATUS.get(status, status)}")
@@ -95,6 +114,8 @@ _SIGNATURES = {
     "kv_attention_workspace_size": [_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)],
     "kv_attention": [_P, _P, _P, _I64, _I64, _I, _P, _I64, _P, ctypes.c_float, _I64, _P, _SZ, _P],
     "draft_verify": [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P],
+    "kv_plan": [_P, _P, _P, _P, _P, _I64, _P, _P, _P],
+    "token_probs": [_P, _I, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I, _P],
     "mnb_unpack_codes": [_P, _I64, _I64, _I, _I, _P, _P],
     "mnb_pack_codes": [_P, _I64, _I64, _I, _I, _P, _P],
     "mnb_quantize_int3": [_P, _I, _I64, _I64, _I, _P, _P, _I, _P],
@@ -484,6 +505,56 @@ def kv_step(seq_lens, page_table, new_start=None, tokens=None, max_new=1) -> KvS
     return d
 
 
+def kv_pool(held, page_table, free_pages, free_count, page_size, *, held_out=None, free_count_out=None) -> KvPoolDesc:
+    """Describes a pool of pages: held int32 [batch], page_table int32 [batch, max_pages] (unit stride along pages),
+    free_pages int32 [num_pages] (a stack, the last free page on top), free_count int32 [1].  held_out and
+    free_count_out get the state after a step (None: held and free_count themselves)."""
+    import torch
+    i32, batch = torch.int32, held.shape[0]
+    device = _device_of(held, "held")
+    if page_table.dim() != 2 or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [batch, max_pages] with unit stride along the pages")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [num_pages]")
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    columns = page_table.shape[1]
+    d = KvPoolDesc(_packed(held, "held", i32, device, (batch,)), _on_gpu(page_table, "page_table", i32, device),
+                   page_table.stride(0) if batch > 1 else max(columns, 1), _packed(free_pages, "free_pages", i32, device),
+                   _packed(free_count, "free_count", i32, device, (1,)), _packed(held_out, "held_out", i32, device, (batch,)),
+                   _packed(free_count_out, "free_count_out", i32, device, (1,)), batch, columns, free_pages.shape[0],
+                   page_size)
+    d.tensors, d.device = (held, page_table, free_pages, free_count, held_out, free_count_out), device
+    return d
+
+
+def kv_plan(pool, keep, new, seq_lens, new_start, *, slots=None, max_tokens=None, refused=None, stream=None, check=True):
+    """Plans a step: each sequence keeps its first keep int32 [batch] tokens and gets new int32 [batch] more.  Writes
+    seq_lens int32 [batch] and new_start int32 [batch + 1] for kv_step, page tables and free pages in the pool, slots
+    int64 [max_tokens] (page * page_size + row of each new token) and refused int32 [batch].  max_tokens: the most new
+    tokens of the step (default: the slots' length, without slots 2^30)."""
+    import torch
+    i32, shape, device = torch.int32, (pool.batch,), keep.get_device()
+    if pool.device != device:
+        _described(device, pool)
+    sp = None
+    if slots is not None:
+        sp = _packed(slots, "slots", torch.int64, device)
+        if max_tokens is None:
+            max_tokens = slots.numel()
+        elif max_tokens > slots.numel():
+            raise ValueError("slots must have max_tokens elements")
+    elif max_tokens is None:
+        max_tokens = 1 << 30
+    st = load_library().kv_plan(_address(pool), _packed(keep, "keep", i32, device, shape),
+                                _packed(new, "new", i32, device, shape), _packed(seq_lens, "seq_lens", i32, device, shape),
+                                _packed(new_start, "new_start", i32, device, (pool.batch + 1,)), max_tokens, sp,
+                                _packed(refused, "refused", i32, device, shape), _stream_on(device, stream))
+    if check:
+        _check(st, "kv_plan")
+    return st
+
+
 def kv_rope(cos_sin=None, *, interleaved=False, q_norm=None, k_norm=None, eps=1e-6) -> KvRopeDesc:
     """Describes the rotation (cos_sin f32 [max_pos, rot_dim]: cosines, then sines) and the per-head norms (f32
     [head_dim]) of queries and keys; None leaves a part out."""
@@ -603,6 +674,97 @@ def kv_attention(cache, step, q, out, workspace=None, *, scale=None, window=0, l
                                      _stream_on(device, stream))
     if check:
         _check(st, "kv_attention")
+    return st
+
+
+def token_rules(*, batch=None, temperature=None, history=None, history_lens=None, prompt_lens=None, repetition=None,
+                frequency=None, presence=None, bias_tokens=None, bias_values=None) -> TokenRules:
+    """Describes what changes a batch's logits: temperature, repetition, frequency, presence f32 [batch]; history int32
+    [batch, columns] (unit stride along the tokens) with history_lens and prompt_lens int32 [batch]; bias_tokens int32
+    and bias_values f32 [batch, biases] of one layout.  None leaves a part out; `batch` is needed where all are None."""
+    import torch
+    given = [t for t in (temperature, history, history_lens, prompt_lens, repetition, frequency, presence, bias_tokens,
+                         bias_values) if t is not None]
+    device = _device_of(given[0], "a tensor of the rules") if given else None
+    if batch is None:
+        if not given:
+            raise ValueError("batch must be given where there are no rules")
+        batch = given[0].shape[0]
+    if (history is None) != (history_lens is None) or (history is None and prompt_lens is not None):
+        raise ValueError("history and history_lens belong together, prompt_lens needs them")
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values belong together")
+    f32, i32 = torch.float32, torch.int32
+
+    def numbers(t, name, dtype=f32):
+        return _packed(t, name, dtype, device, (batch,))
+
+    def rows(t, name, dtype):
+        if t is None:
+            return None, 0, 0
+        if t.dim() != 2 or t.shape[0] != batch or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [batch, any] with unit stride along a row")
+        return _on_gpu(t, name, dtype, device), (t.stride(0) if batch > 1 else t.shape[1]), t.shape[1]
+
+    hp, hs, columns = rows(history, "history", i32)
+    tp, ts, biases = rows(bias_tokens, "bias_tokens", i32)
+    vp, vs, values = rows(bias_values, "bias_values", f32)
+    if (ts, biases) != (vs, values):
+        raise ValueError("bias_tokens and bias_values must have one shape and layout")
+    if columns == 0:
+        hp = None
+    d = TokenRules(numbers(temperature, "temperature"), hp, hs, numbers(history_lens, "history_lens", i32),
+                   numbers(prompt_lens, "prompt_lens", i32), numbers(repetition, "repetition"),
+                   numbers(frequency, "frequency"), numbers(presence, "presence"), tp, vp, ts, batch, columns, biases)
+    d.tensors = (temperature, history, history_lens, prompt_lens, repetition, frequency, presence, bias_tokens, bias_values)
+    d.device = device
+    return d
+
+
+def token_probs(logits, rules, out, *, row_start=None, draft_tokens=None, mask=None, softmax=True, stream=None, check=True):
+    """Writes to out f32 [batch, rows, vocab] the probabilities of a step's logits (softmax=False: the changed logits)
+    under `rules`: logits f32, f16 or bf16 [batch, rows, vocab], or [tokens, vocab] with row_start int32 [batch + 1]
+    (row i of sequence b is row_start[b] + i).  draft_tokens int32 [batch, rows - 1]: row i follows the first i of
+    them.  mask int32 [batch, rows, ceil(vocab / 32)]: bits of the allowed tokens.  Unit stride along the vocabulary;
+    out may be fp32 logits."""
+    import torch
+    batch, rows, vocab = out.shape
+    device = out.get_device()
+    if rules.batch != batch:
+        raise ValueError(f"out must have the rules' batch of {rules.batch} sequences")
+    if rules.device != device and rules.device is not None:
+        _described(device, rules)
+
+    def rows_of(t, name, dtype, width):  # pointer and strides (those of an extent of one are never used)
+        s0, s1, s2 = t.stride()
+        if s2 != 1 and width > 1:
+            raise ValueError(f"{name} must have unit stride along its rows")
+        return _on_gpu(t, name, dtype, device), (s0 if batch > 1 else rows * width), (s1 if rows > 1 else width)
+
+    tokens = 0
+    if row_start is None:
+        if logits.shape != out.shape:
+            raise ValueError(f"logits must be {list(out.shape)}, or [tokens, vocab] with row_start")
+        lp, ls, lr = rows_of(logits, "logits", None, vocab)
+    else:
+        if logits.dim() != 2 or logits.shape[1] != vocab or (vocab > 1 and logits.stride(1) != 1):
+            raise ValueError("logits must be [tokens, vocab] with unit stride along the vocabulary")
+        tokens = logits.shape[0]
+        lp, ls, lr = _on_gpu(logits, "logits", None, device), 0, (logits.stride(0) if tokens > 1 else vocab)
+    op, os_, orow = rows_of(out, "out", torch.float32, vocab)
+    mp, ms, mr = None, 0, 0
+    if mask is not None:
+        words = (vocab + 31) // 32
+        if mask.shape != (batch, rows, words):
+            raise ValueError(f"mask must be {[batch, rows, words]}")
+        mp, ms, mr = rows_of(mask, "mask", torch.int32, words)
+    st = load_library().token_probs(lp, _dtype_code(logits), ls, lr,
+                                    _packed(row_start, "row_start", torch.int32, device, (batch + 1,)), tokens,
+                                    _address(rules),
+                                    _packed(draft_tokens, "draft_tokens", torch.int32, device, (batch, rows - 1)), mp, ms,
+                                    mr, rows, vocab, op, os_, orow, int(bool(softmax)), _stream_on(device, stream))
+    if check:
+        _check(st, "token_probs")
     return st
 
 

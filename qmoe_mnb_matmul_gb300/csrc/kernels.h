@@ -54,6 +54,48 @@ inline cudaError_t launch_ready(dim3 grid, dim3 block, size_t smem, cudaStream_t
     return launch_ex(Kern, grid, block, smem, stream, pdl, args...);
 }
 
+// launch_ready of a kernel in clusters of `cluster` CTAs (up to 16) along x, with `smem` bytes
+// of dynamic shared memory out of at most `most_smem`.
+template <auto Kern, typename... Args>
+inline cudaError_t launch_cluster(dim3 grid, dim3 block, unsigned cluster, size_t smem, size_t most_smem,
+                                  cudaStream_t stream, bool pdl, const Args&... args) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    auto launch = [&] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, Kern, args...);
+    };
+    if (done.load(std::memory_order_relaxed) & bit) {
+        if ((e = launch()) == cudaSuccess) return e;
+        cudaGetLastError();
+    }
+    if (most_smem > 0)
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most_smem));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 static_cast<int>(cudaSharedmemCarveoutMaxShared));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return launch();
+}
+
 // ------------------------------------------------------------- SIMT GEMV
 // Y[M, N] = A[M, K] . W^T for small M, streaming packed rows through shared memory.
 struct GemvArgs {

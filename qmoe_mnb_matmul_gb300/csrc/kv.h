@@ -16,6 +16,11 @@ struct KvCache {
     void* v;
     int64_t num_pages, page_stride, head_stride, token_stride;  // strides in elements
     int page_size, heads, dim, dtype;
+    // 8-bit codes: the scale of a block of 2^block_shift rows of (page, head) is at page *
+    // scale_page_stride + head * scale_head_stride + row / 2^block_shift
+    float *k_scale, *v_scale;
+    int64_t scale_page_stride, scale_head_stride;
+    int block_shift;
 };
 
 // One step's tokens (device arrays of the caller).
@@ -144,5 +149,58 @@ struct DraftArgs {
 };
 cudaError_t launch_draft_verify(const DraftArgs& a, int sm_count, bool pdl, cudaStream_t stream);
 cudaError_t draft_take_error(unsigned int* out);
+
+// --------------------------------------------------------------- kv_plan
+
+constexpr int kKvPlanMaxBatch = 8192;  // sequences whose sums fit in shared memory
+
+struct KvPlanArgs {
+    const int *held, *keep, *add;  // [batch]
+    const int* free_count;
+    int* page_table;               // [batch, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int* free_pages;               // [num_pages], a stack
+    int batch, max_pages, page_size, num_pages;
+    FastDiv by_page;
+    uint32_t max_tokens;
+    int *held_out, *free_count_out, *seq_lens, *new_start;
+    int* refused;                  // [batch] or null
+    int64_t* slots;                // [max_tokens] or null
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, int sm_count, bool pdl, cudaStream_t stream);
+cudaError_t kv_plan_take_error(unsigned int* out);
+
+// ----------------------------------------------------------- token_probs
+
+constexpr int64_t kProbMostSmem = 225 * 1024;
+
+struct ProbArgs {
+    const void* logits;
+    int64_t logits_seq, logits_row;  // elements between sequences, rows
+    const int* row_start;            // [batch + 1] or null: row i of sequence b is row_start[b] + i of `tokens`
+    int64_t tokens;
+    const float* temperature;        // [batch] or null, like the next three
+    const float *repetition, *frequency, *presence;
+    const int* history;              // [batch, history_columns], rows history_stride apart, or null
+    int64_t history_stride;
+    int history_columns;
+    const int *history_lens, *prompt_lens;
+    const int* bias_tokens;          // [batch, biases], rows bias_stride apart
+    const float* bias_values;
+    int64_t bias_stride;
+    int biases;
+    const int* draft_tokens;         // [batch, rows - 1] or null
+    const uint32_t* mask;            // words of a row adjacent, or null
+    int64_t mask_seq, mask_row;
+    int64_t batch, vocab;
+    int rows;
+    float* out;
+    int64_t out_seq, out_row;
+    int softmax;
+};
+// Bytes of a CTA's counts and biases.
+int64_t token_probs_smem(int64_t vocab, bool counts, bool biases, int cluster);
+cudaError_t launch_token_probs(const ProbArgs& a, int dtype, bool pdl, cudaStream_t stream);
+cudaError_t token_probs_take_error(unsigned int* out);
 
 }  // namespace mnb

@@ -1,5 +1,5 @@
-// kv_api.cu -- the extern "C" entry points of the paged key-value cache and of
-// the draft verification: host-side metadata validation (payloads are never read
+// kv_api.cu -- the extern "C" entry points of the paged key-value cache, its plan,
+// the token probabilities and the draft verification: host-side metadata validation (payloads are never read
 // on the host) and launches on the caller's stream.
 #include <cmath>
 
@@ -190,6 +190,126 @@ mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, co
     if (sms <= 0) return MNB_ERR_CUDA;
     return from_cuda(launch_kv_attention(a, dtype, step->max_new, workspace, sms, pdl_enabled(),
                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mnb_status kv_plan(const kv_pool_desc* pool, const int32_t* keep, const int32_t* add, int32_t* seq_lens,
+                   int32_t* new_start, int64_t max_tokens, int64_t* slots, int32_t* refused, mnb_stream_t stream) {
+    if (!pool || pool->batch < 0 || pool->num_pages < 0 || pool->page_size < 1 || max_tokens < 0)
+        return MNB_ERR_INVALID_ARG;
+    if (!pool->free_count || !pool->free_count_out || !new_start || (pool->num_pages > 0 && !pool->free_pages))
+        return MNB_ERR_INVALID_ARG;
+    if (pool->batch > 0 && (!pool->held || !pool->held_out || !pool->page_table || !keep || !add || !seq_lens ||
+                            pool->max_pages < 1 || pool->table_stride < pool->max_pages))
+        return MNB_ERR_INVALID_ARG;
+    if (pool->batch > kKvPlanMaxBatch) return MNB_ERR_UNSUPPORTED;
+    if (max_tokens > (int64_t(1) << 30)) return MNB_ERR_SIZE_OVERFLOW;
+    for (const void* p : {static_cast<const void*>(pool->held), static_cast<const void*>(pool->page_table),
+                          static_cast<const void*>(pool->free_pages), static_cast<const void*>(pool->free_count),
+                          static_cast<const void*>(pool->held_out), static_cast<const void*>(pool->free_count_out),
+                          static_cast<const void*>(keep), static_cast<const void*>(add),
+                          static_cast<const void*>(seq_lens), static_cast<const void*>(new_start),
+                          static_cast<const void*>(refused)})
+        if (!aligned(p, 4)) return MNB_ERR_UNSUPPORTED;
+    if (!aligned(slots, 8)) return MNB_ERR_UNSUPPORTED;
+    int64_t total = 0;
+    if (!span_ok(pool->batch, pool->table_stride, &total)) return MNB_ERR_SIZE_OVERFLOW;
+    KvPlanArgs a = {};
+    a.held = pool->held;
+    a.keep = keep;
+    a.add = add;
+    a.free_count = pool->free_count;
+    a.page_table = pool->page_table;
+    a.table_stride = pool->table_stride;
+    a.free_pages = pool->free_pages;
+    a.batch = pool->batch;
+    a.max_pages = pool->max_pages;
+    a.page_size = pool->page_size;
+    a.num_pages = pool->num_pages;
+    a.max_tokens = static_cast<uint32_t>(max_tokens);
+    a.held_out = pool->held_out;
+    a.free_count_out = pool->free_count_out;
+    a.seq_lens = seq_lens;
+    a.new_start = new_start;
+    a.refused = refused;
+    a.slots = slots;
+    const int sms = sm_count_current();
+    if (sms <= 0) return MNB_ERR_CUDA;
+    return from_cuda(launch_kv_plan(a, sms, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_stride, int64_t logits_row_stride,
+                       const int32_t* row_start, int64_t tokens, const token_rules* rules,
+                       const int32_t* draft_tokens, const uint32_t* mask, int64_t mask_seq_stride,
+                       int64_t mask_row_stride, int64_t rows, int64_t vocab, float* out, int64_t out_seq_stride,
+                       int64_t out_row_stride, int softmax, mnb_stream_t stream) {
+    if (!rules || !valid_dtype(dtype) || rules->batch < 0 || rows < 1 || vocab < 1 || rules->history_columns < 0 ||
+        rules->biases < 0 || tokens < 0)
+        return MNB_ERR_INVALID_ARG;
+    const int64_t batch = rules->batch;
+    if (batch == 0) return MNB_OK;
+    if ((!logits && !(row_start && tokens == 0)) || !out) return MNB_ERR_INVALID_ARG;
+    if (rules->history && (!rules->history_lens || rules->history_stride < rules->history_columns)) return MNB_ERR_INVALID_ARG;
+    if (rules->biases > 0 && (!rules->bias_tokens || !rules->bias_values || rules->bias_stride < rules->biases))
+        return MNB_ERR_INVALID_ARG;
+    // rows that are only read may be shared
+    if (logits_row_stride < 0 || logits_seq_stride < 0 || mask_seq_stride < 0 || mask_row_stride < 0) return MNB_ERR_INVALID_ARG;
+    if ((rows > 1 && out_row_stride < vocab) || (batch > 1 && out_seq_stride < vocab)) return MNB_ERR_INVALID_ARG;
+    if (vocab >= (int64_t(1) << 22) || rows > 1025) return MNB_ERR_UNSUPPORTED;
+    const bool drafts = draft_tokens != nullptr && rows > 1;
+    if (token_probs_smem(vocab, rules->history || drafts, rules->biases > 0, 16) > kProbMostSmem) return MNB_ERR_UNSUPPORTED;
+    if (batch * rows > kMaxInt / 16) return MNB_ERR_SIZE_OVERFLOW;
+    for (const void* p : {static_cast<const void*>(row_start), static_cast<const void*>(rules->temperature),
+                          static_cast<const void*>(rules->history), static_cast<const void*>(rules->history_lens),
+                          static_cast<const void*>(rules->prompt_lens), static_cast<const void*>(rules->repetition),
+                          static_cast<const void*>(rules->frequency), static_cast<const void*>(rules->presence),
+                          static_cast<const void*>(rules->bias_tokens), static_cast<const void*>(rules->bias_values),
+                          static_cast<const void*>(draft_tokens), static_cast<const void*>(mask),
+                          static_cast<const void*>(out)})
+        if (!aligned(p, 4)) return MNB_ERR_UNSUPPORTED;
+    if (!aligned(logits, dsize(dtype))) return MNB_ERR_UNSUPPORTED;
+    int64_t total = 0;
+    if (row_start ? !span_ok(tokens, logits_row_stride, &total)
+                  : !span_ok(batch, logits_seq_stride, &total) || !span_ok(rows, logits_row_stride, &total))
+        return MNB_ERR_SIZE_OVERFLOW;
+    total = 0;
+    if (!span_ok(batch, out_seq_stride, &total) || !span_ok(rows, out_row_stride, &total)) return MNB_ERR_SIZE_OVERFLOW;
+    total = 0;
+    if (!span_ok(batch, mask_seq_stride, &total) || !span_ok(rows, mask_row_stride, &total)) return MNB_ERR_SIZE_OVERFLOW;
+    total = 0;
+    if (!span_ok(batch, rules->history_stride, &total) || !span_ok(batch, rules->bias_stride, &total))
+        return MNB_ERR_SIZE_OVERFLOW;
+    ProbArgs a = {};
+    a.logits = logits;
+    a.logits_seq = logits_seq_stride;
+    a.logits_row = logits_row_stride;
+    a.row_start = row_start;
+    a.tokens = tokens;
+    a.temperature = rules->temperature;
+    a.repetition = rules->repetition;
+    a.frequency = rules->frequency;
+    a.presence = rules->presence;
+    a.history = rules->history;
+    a.history_stride = rules->history_stride;
+    a.history_columns = rules->history_columns;
+    a.history_lens = rules->history_lens;
+    a.prompt_lens = rules->prompt_lens;
+    a.bias_tokens = rules->bias_tokens;
+    a.bias_values = rules->bias_values;
+    a.bias_stride = rules->bias_stride;
+    a.biases = rules->biases;
+    a.draft_tokens = drafts ? draft_tokens : nullptr;
+    a.mask = mask;
+    a.mask_seq = mask_seq_stride;
+    a.mask_row = mask_row_stride;
+    a.batch = batch;
+    a.vocab = vocab;
+    a.rows = static_cast<int>(rows);
+    a.out = out;
+    a.out_seq = out_seq_stride;
+    a.out_row = out_row_stride;
+    a.softmax = softmax != 0;
+    if (sm_count_current() <= 0) return MNB_ERR_CUDA;
+    return from_cuda(launch_token_probs(a, dtype, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 mnb_status draft_verify(const float* target, int64_t target_seq_stride, int64_t target_row_stride, const float* draft,
