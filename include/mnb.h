@@ -85,7 +85,8 @@ typedef enum {
                                   mnb_quantize_int3 rejected (device error word) */
 } mnb_status;
 
-typedef enum { MNB_F32 = 0, MNB_F16 = 1, MNB_BF16 = 2 } mnb_dtype;
+/* MNB_E4M3 (8-bit codes with scales) is a key-value cache's alone. */
+typedef enum { MNB_F32 = 0, MNB_F16 = 1, MNB_BF16 = 2, MNB_E4M3 = 3 } mnb_dtype;
 
 /* Row order of a fused FC1 weight of 2I rows: INTERLEAVED puts gate_i at row 2i
  * and up_i at row 2i+1 (the fused interleaved gate/up of "INT3 QMoE CUDA
@@ -351,13 +352,23 @@ mnb_status qmoe_permute(const int32_t* topk_idx, int64_t T, int k, int64_t E, in
  * k and a v interleaved in one buffer are all described.  dtype f16 or bf16;
  * head_dim a multiple of 8 in 16..256; page_size a multiple of 8; k, v and
  * the strides in whole 16-byte units.  The pages quoted above have no cache:
- * these entry points exist for decoders built on the products. */
+ * these entry points exist for decoders built on the products.
+ * dtype MNB_E4M3: elements are 8-bit codes (e4m3: finite up to 448, no
+ * infinities), element = code * scale with an fp32 scale (finite, not negative)
+ * for each block of scale_block rows of a page and head: k_scale or v_scale at
+ * page * scale_page_stride + head * scale_head_stride + row / scale_block.
+ * scale_block a power of two in 8..128 that divides page_size; head_dim and the
+ * strides multiples of 16.  The scale fields are read for this dtype alone. */
 typedef struct {
     void* k;
     void* v;
     int64_t num_pages, page_stride, head_stride, token_stride;
     int32_t page_size, kv_heads, head_dim;
     int32_t dtype; /* mnb_dtype */
+    float* k_scale;
+    float* v_scale;
+    int64_t scale_page_stride, scale_head_stride;
+    int32_t scale_block;
 } kv_cache_desc;
 
 /* The tokens of one step of a batch of sequences (device arrays; kept by the
@@ -455,7 +466,7 @@ typedef struct {
 /* Stores a step's keys and values in the cache and writes its queries to
  * q_out, keys and queries normed and rotated as *rope says (NULL: neither).
  * q [tokens, q_heads, head_dim], k and v [tokens, kv_heads, head_dim] in dtype
- * (f32 or the cache's), each with its own stride in elements between tokens,
+ * (f32 or the cache's; any over 8-bit codes), each with its own stride in elements between tokens,
  * so that they may be parts of one projection's output rows; q_out like q, and
  * may be q itself.  q and q_out may both be NULL.  Computed in fp32, rounded
  * once to the cache's dtype (q_out: to dtype; what an fp16 cache cannot hold
@@ -463,7 +474,16 @@ typedef struct {
  * outside [0, num_pages), a position past max_pages * page_size) or no row of
  * cos_sin is skipped, with its q_out row, and records MNB_ERR_CONTENT in the
  * device error word.  Pointers and strides in whole 16-byte units (strides:
- * multiples of 8 elements). */
+ * multiples of 8 elements).
+ * 8-bit codes: with a the largest finite magnitude among the step's tokens in a
+ * block, need = the smallest power of two s >= 2^-126 with a <= 448 s (0 for a =
+ * 0).  The block's scale becomes need, or stays where the block holds older
+ * tokens of the sequence (rows before the step's first) and their scale is at
+ * least that; where it grows, the older codes become code * old scale / new
+ * scale.  A code is value / scale to the nearest, ties to even; 0 where the scale
+ * is 0, NaN for a value that is not finite.  Rows behind the last new token keep
+ * their codes.  A page that other sequences share holds whole blocks, or is
+ * appended to by one of them. */
 mnb_status kv_append(const kv_cache_desc* cache, const kv_step_desc* step, const kv_rope_desc* rope, const void* q,
                      int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, mnb_dtype dtype, void* q_out, int64_t q_out_stride, mnb_stream_t stream);

@@ -7,7 +7,7 @@ sm_103a kernels behind the C ABI of ``include/mnb.h``); this package is its
 thin ctypes binding.  Build it with ``__graft_entry__.build()`` or
 ``python -m qmoe_mnb_matmul_gb300._build``.
 """
-from ._binding import (BF16, F16, F32, FC1_CONCAT, FC1_INTERLEAVED, KvCacheDesc, KvPoolDesc,  # noqa: F401
+from ._binding import (BF16, E4M3, F16, F32, FC1_CONCAT, FC1_INTERLEAVED, KvCacheDesc, KvPoolDesc,  # noqa: F401
                        KvRopeDesc, KvStepDesc, MnbError, PrepackedDesc, QmoeOptions, TokenRules, draft_verify,
                        header_functions, kv_append, kv_attention, kv_attention_workspace_size, kv_cache, kv_plan,
                        kv_pool, kv_rope, kv_step, library_path,

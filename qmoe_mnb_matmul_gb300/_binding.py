@@ -23,6 +23,7 @@ HEADER = os.path.join(ROOT, "include", "mnb.h")
 STATUS = {0: "MNB_OK", 1: "MNB_ERR_INVALID_ARG", 2: "MNB_ERR_UNSUPPORTED", 3: "MNB_ERR_SIZE_OVERFLOW",
           4: "MNB_ERR_WORKSPACE", 5: "MNB_ERR_CUDA", 6: "MNB_ERR_TIMEOUT", 7: "MNB_ERR_CONTENT"}
 F32, F16, BF16 = 0, 1, 2
+E4M3 = 3  # of a key-value cache alone
 FC1_INTERLEAVED, FC1_CONCAT = 0, 1
 
 
@@ -40,7 +41,9 @@ class KvCacheDesc(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("dtype", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_block", ctypes.c_int32)]
     device = None  # of the tensors, where kv_cache saw them
 
 
@@ -468,17 +471,33 @@ def _described(device, *descriptors):
             raise ValueError(f"{type(d).__name__} of tensors on CUDA device {d.device}, not on {device} like the others")
 
 
-def kv_cache(k, v) -> KvCacheDesc:
+def kv_cache(k, v, k_scale=None, v_scale=None) -> KvCacheDesc:
     """Describes a paged cache held in k and v [pages, kv_heads, page_size, head_dim] (f16 or bf16; any strides
-    with unit stride along head_dim, the same for both: permuted views describe other layouts)."""
+    with unit stride along head_dim, the same for both: permuted views describe other layouts).  A cache of 8-bit codes
+    has k and v in float8_e4m3fn and k_scale, v_scale f32 [pages, kv_heads, page_size / block]: element = code * scale
+    (any strides with unit stride along the blocks, the same for both)."""
+    import torch
     if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
         raise ValueError("k and v must be 4-D tensors of one shape, dtype and layout")
     if k.stride(3) != 1:
         raise ValueError("the head dimension must have unit stride")
     device = _device_of(k, "k")
+    codes = k.dtype == torch.float8_e4m3fn
+    if codes != (k_scale is not None) or codes != (v_scale is not None):
+        raise ValueError("a cache of float8_e4m3fn has k_scale and v_scale, others have none")
     d = KvCacheDesc(_on_gpu(k, "k", None, device), _on_gpu(v, "v", None, device), k.shape[0], k.stride(0), k.stride(1),
-                    k.stride(2), k.shape[2], k.shape[1], k.shape[3], _dtype_code(k))
-    d.tensors, d.device = (k, v), device  # (the tensors live as long as the descriptor)
+                    k.stride(2), k.shape[2], k.shape[1], k.shape[3], E4M3 if codes else _dtype_code(k))
+    if codes:
+        blocks = k_scale.shape[2] if k_scale.dim() == 3 else 0
+        if k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride() or blocks < 1 or \
+                k_scale.shape != (k.shape[0], k.shape[1], blocks) or k.shape[2] % blocks:
+            raise ValueError("k_scale and v_scale must be [pages, kv_heads, page_size / block], of one layout")
+        if blocks > 1 and k_scale.stride(2) != 1:
+            raise ValueError("the scales must have unit stride along the blocks")
+        d.k_scale, d.v_scale = _on_gpu(k_scale, "k_scale", torch.float32, device), _on_gpu(v_scale, "v_scale", torch.float32, device)
+        d.scale_page_stride, d.scale_head_stride = k_scale.stride(0), k_scale.stride(1)
+        d.scale_block = k.shape[2] // blocks
+    d.tensors, d.device = (k, v, k_scale, v_scale), device  # (the tensors live as long as the descriptor)
     return d
 
 

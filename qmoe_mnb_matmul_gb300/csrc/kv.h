@@ -66,10 +66,14 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream);
 cudaError_t kv_append_take_error(unsigned int* out);
+cudaError_t launch_kv_append8(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream);
+cudaError_t kv_append8_take_error(unsigned int* out);
 
 // ---------------------------------------------------------- kv_attention
 
 constexpr int kKvTile = 64;      // cached tokens per tile
+// over 8-bit codes: twice as many for up to eight rows, as far as a tile's bytes stay the same
+constexpr int kv_tile8(int rows, int pad) { return rows == 8 && pad <= 128 ? 128 : 64; }
 constexpr int kKvMaxCtas = 304;  // CTAs of the main kernel: two on each of 152 SMs
 
 // Division by a number fixed at launch: x / d = (hi32(x m) + x) >> s for 0 <= x < 2^31
@@ -89,8 +93,9 @@ struct FastDiv {
 };
 
 // Attention weights are 2^(score - reference), where the reference is the row's largest
-// score (in log2 units) less this shift: the range that the cache's type leaves free.
-constexpr int kv_weight_shift(int dtype) { return dtype == MNB_F16 ? 15 : 0; }
+// score (in log2 units) less this shift: the range that the weights' type leaves free (fp16
+// over 8-bit codes).
+constexpr int kv_weight_shift(int dtype) { return dtype == MNB_BF16 ? 0 : 15; }
 
 #ifdef __CUDACC__
 // Natural log-sum-exp of a row from its reference and its sum of weights.
@@ -111,6 +116,7 @@ struct KvAttnArgs {
     int group;   // query heads per key-value head
     FastDiv by_group, by_page;  // division by group, by the page size
     float scale;
+    int q_dtype;
     int window;  // 0: every earlier token
     int box_rows;
     // partial results of the pairs split over CTAs: two slots per CTA

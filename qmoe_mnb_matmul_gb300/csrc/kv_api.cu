@@ -22,7 +22,8 @@ bool span_ok(int64_t extent, int64_t stride, int64_t* total) {
 
 mnb_status check_cache(const kv_cache_desc* d, KvCache* c) {
     if (!d || !d->k || !d->v) return MNB_ERR_INVALID_ARG;
-    if (d->num_pages < 1 || d->page_size < 1 || d->kv_heads < 1 || d->head_dim < 1 || !valid_dtype(d->dtype))
+    const bool codes = d->dtype == MNB_E4M3;
+    if (d->num_pages < 1 || d->page_size < 1 || d->kv_heads < 1 || d->head_dim < 1 || !(valid_dtype(d->dtype) || codes))
         return MNB_ERR_INVALID_ARG;
     if (d->dtype == MNB_F32) return MNB_ERR_UNSUPPORTED;
     if (d->head_dim % 8 || d->head_dim < 16 || d->head_dim > 256 || d->page_size % 8) return MNB_ERR_UNSUPPORTED;
@@ -39,9 +40,27 @@ mnb_status check_cache(const kv_cache_desc* d, KvCache* c) {
     c->page_stride = d->num_pages > 1 ? d->page_stride : d->head_dim;
     for (const int64_t s : {c->token_stride, c->head_stride, c->page_stride}) {
         if (s < c->dim) return MNB_ERR_INVALID_ARG;
-        if (s % 8 || s >= (int64_t(1) << 38)) return MNB_ERR_UNSUPPORTED;  // whole 16-byte units, below 2^40 bytes
+        if (s % (codes ? 16 : 8) || s >= (int64_t(1) << 38)) return MNB_ERR_UNSUPPORTED;  // whole 16-byte units, below 2^40 bytes
     }
     if (!aligned(d->k, 16) || !aligned(d->v, 16)) return MNB_ERR_UNSUPPORTED;
+    if (codes) {
+        if (!d->k_scale || !d->v_scale || d->scale_block < 1) return MNB_ERR_INVALID_ARG;
+        if (d->head_dim % 16 || d->scale_block < 8 || d->scale_block > 128 || (d->scale_block & (d->scale_block - 1)) ||
+            d->page_size % d->scale_block || !aligned(d->k_scale, 4) || !aligned(d->v_scale, 4))
+            return MNB_ERR_UNSUPPORTED;
+        const int64_t blocks = d->page_size / d->scale_block;
+        c->k_scale = d->k_scale;
+        c->v_scale = d->v_scale;
+        c->scale_head_stride = d->kv_heads > 1 ? d->scale_head_stride : blocks;
+        c->scale_page_stride = d->num_pages > 1 ? d->scale_page_stride : blocks;
+        c->block_shift = 0;
+        while ((1 << c->block_shift) < d->scale_block) ++c->block_shift;
+        int64_t span = 0;
+        for (const int64_t s : {c->scale_head_stride, c->scale_page_stride})
+            if (s < blocks) return MNB_ERR_INVALID_ARG;
+        if (!span_ok(c->num_pages, c->scale_page_stride, &span) || !span_ok(c->heads, c->scale_head_stride, &span))
+            return MNB_ERR_SIZE_OVERFLOW;
+    }
     int64_t total = 0;
     if (!span_ok(c->num_pages, c->page_stride, &total) || !span_ok(c->heads, c->head_stride, &total) ||
         !span_ok(c->page_size, c->token_stride, &total))
@@ -101,7 +120,7 @@ mnb_status kv_append(const kv_cache_desc* cache, const kv_step_desc* step, const
     bool nothing;
     if ((st = check_step(step, a.cache, &a.step, &nothing)) != MNB_OK) return st;
     if (!valid_dtype(dtype) || (q == nullptr) != (q_out == nullptr) || (q && q_heads < 1)) return MNB_ERR_INVALID_ARG;
-    if (dtype != MNB_F32 && dtype != a.cache.dtype) return MNB_ERR_UNSUPPORTED;
+    if (dtype != MNB_F32 && dtype != a.cache.dtype && a.cache.dtype != MNB_E4M3) return MNB_ERR_UNSUPPORTED;
     if (rope) {
         if (rope->cos_sin) {
             if (rope->max_pos < 1 || rope->rot_dim < 1 || rope->rot_dim > a.cache.dim) return MNB_ERR_INVALID_ARG;
@@ -141,7 +160,8 @@ mnb_status kv_append(const kv_cache_desc* cache, const kv_step_desc* step, const
     a.q_out_stride = q_out_stride;
     const int sms = sm_count_current();
     if (sms <= 0) return MNB_ERR_CUDA;
-    return from_cuda(launch_kv_append(a, sms, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
+    auto launch = a.cache.dtype == MNB_E4M3 ? launch_kv_append8 : launch_kv_append;
+    return from_cuda(launch(a, sms, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_new,
@@ -167,7 +187,7 @@ mnb_status kv_attention(const kv_cache_desc* cache, const kv_step_desc* step, co
     if (!valid_dtype(dtype) || q_heads < 1 || q_heads % a.cache.heads || window < 0 ||
         !(scale > 0.f && std::isfinite(scale)))
         return MNB_ERR_INVALID_ARG;
-    if (dtype != MNB_F32 && dtype != a.cache.dtype) return MNB_ERR_UNSUPPORTED;
+    if (dtype != MNB_F32 && dtype != a.cache.dtype && a.cache.dtype != MNB_E4M3) return MNB_ERR_UNSUPPORTED;
     if (nothing) return MNB_OK;
     if (!q || !out) return MNB_ERR_INVALID_ARG;
     if (q_heads > kMaxInt / (a.cache.dim * 4) || step->tokens > (int64_t(1) << 30) / q_heads) return MNB_ERR_SIZE_OVERFLOW;

@@ -19,6 +19,17 @@ MNB_SLICE_DECL(kv_attention_bf16)
 MNB_SLICE_DECL(kv_attention_f16_qf32)
 MNB_SLICE_DECL(kv_attention_bf16_qf32)
 #undef MNB_SLICE_DECL
+#define MNB_SLICE_DECL(NAME)                                                                                    \
+    cudaError_t NAME(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvAttnArgs& a, int rows,           \
+                     int sm_count, bool pdl, cudaStream_t stream, int* ctas);                                   \
+    cudaError_t NAME##_take_error(unsigned int* out);
+MNB_SLICE_DECL(kv_attention8_q16_64)
+MNB_SLICE_DECL(kv_attention8_q16_128)
+MNB_SLICE_DECL(kv_attention8_q16_256)
+MNB_SLICE_DECL(kv_attention8_qf32_64)
+MNB_SLICE_DECL(kv_attention8_qf32_128)
+MNB_SLICE_DECL(kv_attention8_qf32_256)
+#undef MNB_SLICE_DECL
 
 namespace {
 
@@ -181,16 +192,19 @@ cudaError_t encode_cache(CUtensorMap* map, void* base, const KvCache& c, int box
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
                                 static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride * 2),
-                                   static_cast<cuuint64_t>(c.head_stride * 2),
-                                   static_cast<cuuint64_t>(c.page_stride * 2)};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const int es = c.dtype == MNB_E4M3 ? 1 : 2;
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride * es),
+                                   static_cast<cuuint64_t>(c.head_stride * es),
+                                   static_cast<cuuint64_t>(c.page_stride * es)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     std::memset(map, 0, sizeof *map);
-    const CUresult r = encode(
-        map, c.dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
-        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUtensorMapDataType type = c.dtype == MNB_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c.dtype == kBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = encode(map, type, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorNotSupported;
 }
 
@@ -216,7 +230,10 @@ KvAttnSpace kv_attention_space(int rows, int pad) {
 cudaError_t kv_attention_take_error(unsigned int* out) {
     unsigned int first = 0;
     for (auto take : {kv_attention_f16_take_error, kv_attention_bf16_take_error, kv_attention_f16_qf32_take_error,
-                      kv_attention_bf16_qf32_take_error}) {
+                      kv_attention_bf16_qf32_take_error, kv_attention8_q16_64_take_error,
+                      kv_attention8_q16_128_take_error, kv_attention8_q16_256_take_error,
+                      kv_attention8_qf32_64_take_error, kv_attention8_qf32_128_take_error,
+                      kv_attention8_qf32_256_take_error}) {
         unsigned int v = 0;
         const cudaError_t e = take(&v);
         if (e != cudaSuccess) return e;
@@ -237,17 +254,27 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     a.join = reinterpret_cast<int4*>(ws + sp.join);
     a.by_group.set(static_cast<uint32_t>(a.group));
     a.by_page.set(static_cast<uint32_t>(a.cache.page_size));
+    a.q_dtype = q_dtype;
+    const bool codes = a.cache.dtype == MNB_E4M3;
     // a TMA box holds as many rows as divide a page (at least 8, at most a tile)
-    a.box_rows = kKvTile;
+    a.box_rows = codes ? kv_tile8(rows, pad) : kKvTile;
     while (a.cache.page_size % a.box_rows) a.box_rows >>= 1;
     CUtensorMap kmap, vmap;
     cudaError_t e = encode_cache(&kmap, a.cache.k, a.cache, a.box_rows);
     if (e == cudaSuccess) e = encode_cache(&vmap, a.cache.v, a.cache, a.box_rows);
     if (e != cudaSuccess) return e;
     const bool bf = a.cache.dtype == kBF16, f32 = q_dtype == kF32;
-    auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);
     int ctas = 0;
-    if ((e = slice(kmap, vmap, a, rows, pad, sm_count, pdl, stream, &ctas)) != cudaSuccess) return e;
+    if (codes) {
+        auto slice = pad == 64    ? (f32 ? kv_attention8_qf32_64 : kv_attention8_q16_64)
+                     : pad == 128 ? (f32 ? kv_attention8_qf32_128 : kv_attention8_q16_128)
+                                  : (f32 ? kv_attention8_qf32_256 : kv_attention8_q16_256);
+        e = slice(kmap, vmap, a, rows, sm_count, pdl, stream, &ctas);
+    } else {
+        auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);
+        e = slice(kmap, vmap, a, rows, pad, sm_count, pdl, stream, &ctas);
+    }
+    if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(ctas),
                     static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(rows, a.group * max_new), kJoinGridY)));
     if (pad == 64) return launch_ready<kv_join_kernel<64>>(grid, dim3(128), 0, stream, pdl, a, rows, q_dtype);

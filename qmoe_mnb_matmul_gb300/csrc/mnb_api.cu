@@ -83,7 +83,8 @@ mnb_status mnb_get_last_device_error(mnb_stream_t stream) {
                                               gemm_tc_take_error, quant_take_error, diag_take_error,
                                               qmoe_decode_take_error, kv_append_take_error,
                                               kv_attention_take_error, draft_take_error,
-                                              kv_plan_take_error, token_probs_take_error};
+                                              kv_plan_take_error, token_probs_take_error,
+                                              kv_append8_take_error};
     for (auto take : takers) {
         unsigned int v = 0;
         if (take(&v) != cudaSuccess) return MNB_ERR_CUDA;
