@@ -572,8 +572,11 @@ typedef struct {
  *            is 1 where v is allowed; strides in words (0 shares a row).
  *   out      fp32 [batch, rows, vocab] with strides; may be fp32 logits of the
  *            same strides (without row_start), else no overlap.
- * vocab < 2^22, and no more than 921600 with a history or drafts or with biases,
- * 460800 with both; rows <= 1025; else MNB_ERR_UNSUPPORTED. */
+ * vocab < 2^22; rows <= 1025; history_columns + rows < 2^20; biases <= 2047; and,
+ * with n = history_columns + rows - 1 + biases (what is given of them) and t =
+ * vocab / 16 rounded up to a multiple of 2048, t / 4 + 8 min(n, t) <= 230400 (so
+ * for any n up to 400000 tokens, for any vocabulary up to n = 20000); else
+ * MNB_ERR_UNSUPPORTED. */
 mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_stride, int64_t logits_row_stride,
                        const int32_t* row_start, int64_t tokens, const token_rules* rules,
                        const int32_t* draft_tokens, const uint32_t* mask, int64_t mask_seq_stride,

@@ -179,6 +179,7 @@ cudaError_t kv_plan_take_error(unsigned int* out);
 // ----------------------------------------------------------- token_probs
 
 constexpr int64_t kProbMostSmem = 225 * 1024;
+constexpr int kProbMostHistory = (1 << 20) - 1, kProbMostBiases = 2047;
 
 struct ProbArgs {
     const void* logits;
@@ -204,9 +205,9 @@ struct ProbArgs {
     int64_t out_seq, out_row;
     int softmax;
 };
-// Bytes of a CTA's counts and biases.
-int64_t token_probs_smem(int64_t vocab, bool counts, bool biases, int cluster);
-cudaError_t launch_token_probs(const ProbArgs& a, int dtype, bool pdl, cudaStream_t stream);
+// Whether the lists of a row (history, drafts, biases: `listed` entries at most) fit in a cluster's shared memory.
+bool token_probs_fits(int64_t vocab, int64_t listed);
+cudaError_t launch_token_probs(const ProbArgs& a, int dtype, int sm_count, bool pdl, cudaStream_t stream);
 cudaError_t token_probs_take_error(unsigned int* out);
 
 }  // namespace mnb

@@ -276,7 +276,10 @@ mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_s
     if ((rows > 1 && out_row_stride < vocab) || (batch > 1 && out_seq_stride < vocab)) return MNB_ERR_INVALID_ARG;
     if (vocab >= (int64_t(1) << 22) || rows > 1025) return MNB_ERR_UNSUPPORTED;
     const bool drafts = draft_tokens != nullptr && rows > 1;
-    if (token_probs_smem(vocab, rules->history || drafts, rules->biases > 0, 16) > kProbMostSmem) return MNB_ERR_UNSUPPORTED;
+    const int64_t listed = (rules->history ? rules->history_columns : 0) + (drafts ? rows - 1 : 0) + rules->biases;
+    if (!token_probs_fits(vocab, listed)) return MNB_ERR_UNSUPPORTED;
+    if ((rules->history ? rules->history_columns : 0) + rows > kProbMostHistory || rules->biases > kProbMostBiases)
+        return MNB_ERR_UNSUPPORTED;
     if (batch * rows > kMaxInt / 16) return MNB_ERR_SIZE_OVERFLOW;
     for (const void* p : {static_cast<const void*>(row_start), static_cast<const void*>(rules->temperature),
                           static_cast<const void*>(rules->history), static_cast<const void*>(rules->history_lens),
@@ -328,8 +331,9 @@ mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_s
     a.out_seq = out_seq_stride;
     a.out_row = out_row_stride;
     a.softmax = softmax != 0;
-    if (sm_count_current() <= 0) return MNB_ERR_CUDA;
-    return from_cuda(launch_token_probs(a, dtype, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
+    const int sms = sm_count_current();
+    if (sms <= 0) return MNB_ERR_CUDA;
+    return from_cuda(launch_token_probs(a, dtype, sms, pdl_enabled(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 mnb_status draft_verify(const float* target, int64_t target_seq_stride, int64_t target_row_stride, const float* draft,

@@ -60,12 +60,14 @@ def test_probs_errors(real):
                 dict(biases=3, bias_tokens=FAKE, bias_values=FAKE, bias_stride=2)):
         assert probs(real, **bad) == INVALID, bad
     long = dict(os=1 << 24, orow=1 << 23, ls=1 << 24, lr=1 << 23)
-    past = dict(history=FAKE, history_lens=FAKE, history_columns=5, history_stride=5)
+    lots = dict(history=FAKE, history_lens=FAKE, history_columns=500000, history_stride=500000)
     extra = dict(biases=1, bias_tokens=FAKE, bias_values=FAKE, bias_stride=1)
     for bad in (dict(vocab=1 << 22, **long), dict(rows=1026, os=1 << 21), dict(logits=FAKE + 2), dict(logits=FAKE + 1, dt=1),
                 dict(out=FAKE + 2), dict(start=FAKE + 2, tokens=9), dict(drafts=FAKE + 2), dict(mask=FAKE + 1),
-                dict(temperature=FAKE + 2), dict(presence=FAKE + 2), dict(vocab=921601, **past, **long),
-                dict(vocab=921601, drafts=FAKE, **long), dict(vocab=460801, **past, **extra, **long)):
+                dict(temperature=FAKE + 2), dict(presence=FAKE + 2), dict(vocab=1 << 21, **lots, **long),
+                dict(vocab=460801, **lots, **extra, **long),
+                dict(history=FAKE, history_lens=FAKE, history_columns=1 << 20, history_stride=1 << 20),
+                dict(biases=2048, bias_tokens=FAKE, bias_values=FAKE, bias_stride=2048)):
         assert probs(real, **bad) == UNSUPPORTED, bad
     for bad in (dict(lr=1 << 61), dict(os=1 << 61), dict(mask=FAKE, ms=1 << 61), dict(batch=1 << 26),
                 dict(start=FAKE, tokens=1 << 40, lr=1 << 40)):
