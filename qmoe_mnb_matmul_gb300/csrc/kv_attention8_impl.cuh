@@ -28,8 +28,8 @@
 // fp32 (22 bits, elements below 2^-17 of the largest err by 2^-39 of it).  Weights are
 // 2^15 times as large and in two fp16 parts, as over an fp16 cache: 22 bits down to 2^-28
 // of the row's largest so far, 16 to 2^-34, an error of 2^-51 of the largest below.  A
-// warp's tokens of a tile take their weights times b_j / b (b the largest of their
-// scales; up to 16, 32 or 64 tokens share one) into the product, and the product is
+// warp's tokens of a tile take their weights times b_j / b (b the power of two above the
+// largest of their scales; up to 16, 32 or 64 tokens share one) into the product, and the product is
 // multiplied by b: a block whose scale is far below its neighbours' loses what that
 // ratio takes from the 2^-51.
 #pragma once
@@ -63,6 +63,11 @@ struct Plan8 {
     static constexpr int kBytes = 1024 + kSlots * kSlotBytes + kQBytes + kMergeBytes;
     static_assert(kSlots >= 2, "a key tile and a value tile must fit");
 };
+
+// What a pair costs besides its tiles, in tiles: its queries, the first tile's way, the
+// join of the warps, the store (64 sequences of 1 .. 8192 tokens: 136 us with none, 117
+// with one, 107 with two, 99 with three, 97 with four; 8 of 2000: 15.0 with three, 15.5 with four).
+constexpr int kPairUnits = 3;
 
 // Two codes (the low 16 bits) as fp16.
 __device__ __forceinline__ uint32_t halves(uint32_t codes) {
@@ -189,7 +194,10 @@ __device__ __forceinline__ void produce8(const KvAttnArgs& a, const CUtensorMap*
         }
         at += nt * w.t.cost;
         w.tile += nt;
-        if (at < r.end) next_pair<ROWS, TILE>(a, w);
+        if (at < r.end) {
+            next_pair<ROWS, TILE>(a, w);
+            at += kPairUnits;
+        }
     }
     // a page number outside the cache: its tokens read as zeros; or a length past the page table
     if (bad) record_error(MNB_ERR_CONTENT);
@@ -475,14 +483,16 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                         }
                 }
         }
-        // the warp's largest value scale, and the others over it
+        // a power of two above the warp's largest value scale, and the scales over it
         float b = 0.f;
 #pragma unroll
         for (int t = 0; t < MT; ++t) b = fmaxf(b, fmaxf(vb[t][0], vb[t][1]));
+        const uint32_t be = min(__float_as_uint(b) >> 23, 252u);
+        b = __uint_as_float((be + 1u) << 23);
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) vb[t][y] = b > 0.f ? __fdiv_rn(vb[t][y], b) : 0.f;
+            for (int y = 0; y < 2; ++y) vb[t][y] *= __uint_as_float((253u - be) << 23);
         float f[RG][2];
         uint32_t pb[MT][RG][PP][2];  // P^T in fp16 parts, as the B operand
 #pragma unroll
@@ -610,10 +620,16 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
                     for (int g = 0; g < RG; ++g)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float sum = fmaf(z[1][g][x], 1.f / kF16Up, z[0][g][x]);
-                            float& to = o[2 * np + y][g][x];
-                            to = fmaf(sum, b, to * f[g][x & 1]);
+                        for (int x = 0; x < 4; x += 2) {  // (packed fp32 instructions)
+                            float (&to)[4] = o[2 * np + y][g];
+                            const float2 sum = ffma2(make_float2(z[1][g][x], z[1][g][x + 1]),
+                                                     make_float2(1.f / kF16Up, 1.f / kF16Up),
+                                                     make_float2(z[0][g][x], z[0][g][x + 1]));
+                            const float2 old = ffma2(make_float2(to[x], to[x + 1]), make_float2(f[g][0], f[g][1]),
+                                                     make_float2(0.f, 0.f));
+                            const float2 now = ffma2(sum, make_float2(b, b), old);
+                            to[x] = now.x;
+                            to[x + 1] = now.y;
                         }
                 }
             }
@@ -759,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
     grid_launch_dependents();
 
     Walk w = {};
-    const Range r = find_range<ROWS, TILE>(a, w);
+    const Range r = find_range<ROWS, TILE, kPairUnits>(a, w);
     if (warp == kComputeWarps) {
         produce8<DP, ROWS, QF32, KSLOTS, true>(a, &kmap, sm.k, scales, k_full, k_empty, w, r);
         return;
@@ -804,7 +820,10 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
         }
         at += nt * w.t.cost;
         w.tile += nt;
-        if (at < r.end) next_pair<ROWS, TILE>(a, w);
+        if (at < r.end) {
+            next_pair<ROWS, TILE>(a, w);
+            at += kPairUnits;
+        }
     }
     if (warp == 0 && lane == 0) a.join[blockIdx.x] = join;
 }

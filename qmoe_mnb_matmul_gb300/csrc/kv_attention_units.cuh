@@ -199,14 +199,15 @@ __device__ __forceinline__ void load_sequence(const KvAttnArgs& a, Walk& w, int 
     w.row_tiles = (w.count * a.group + ROWS - 1) / ROWS;
 }
 
-// Units of the sequence in w over all its row tiles, for one key-value head.
-template <int ROWS, int TILE>
+// Units of the sequence in w over all its row tiles, for one key-value head: those of its
+// tiles, and PAIR more ahead of each row tile's for what a pair costs by itself.
+template <int ROWS, int TILE, int PAIR>
 __device__ __forceinline__ int64_t sequence_units(const KvAttnArgs& a, const Walk& w) {
     int64_t n = 0;
 #pragma unroll 1
     for (int rt = 0; rt < w.row_tiles; ++rt) {
         const RowTile t = row_tile<ROWS, TILE>(a, w.count, w.pos0, rt);
-        n += t.tiles * t.cost;
+        n += t.tiles * t.cost + PAIR;
     }
     return n;
 }
@@ -262,7 +263,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {
 // the range begins in again.  The way from the launch to the first copy passes
 // through here, so it is short rather than general: with up to 32 sequences one load
 // of lengths, two 32-bit divisions (one of the units, one of the pair).
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int PAIR = 0>
 __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     const int lane = threadIdx.x & 31, batch = a.step.batch, per = (batch + 31) / 32;
     const int64_t heads = a.cache.heads;
@@ -271,7 +272,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
 #pragma unroll 4
     for (int s = lane * per; s < min((lane + 1) * per, batch); ++s) {
         load_sequence<ROWS>(a, mine, s);
-        units += sequence_units<ROWS, TILE>(a, mine);
+        units += sequence_units<ROWS, TILE, PAIR>(a, mine);
     }
     units *= heads;
     int64_t incl = warp_scan(units);
@@ -298,7 +299,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
             units = 0;
             if (s0 + lane < last) {
                 load_sequence<ROWS>(a, mine, s0 + lane);
-                units = sequence_units<ROWS, TILE>(a, mine) * heads;
+                units = sequence_units<ROWS, TILE, PAIR>(a, mine) * heads;
             }
             incl = before + warp_scan(units);
             begin = incl - units;
@@ -319,11 +320,11 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
 #pragma unroll 1
     for (w.rt = 0;; ++w.rt) {
         w.t = row_tile<ROWS, TILE>(a, w.count, w.pos0, w.rt);
-        const int64_t n = static_cast<int64_t>(w.t.tiles) * w.t.cost * heads;
+        const int64_t n = (static_cast<int64_t>(w.t.tiles) * w.t.cost + PAIR) * heads;
         if (off < n) break;
         off -= n;
     }
-    const int pair = w.t.tiles * w.t.cost;  // units of a pair: below 2^27
+    const int pair = w.t.tiles * w.t.cost + PAIR;  // units of a pair: below 2^28
     if (off < (int64_t(1) << 31)) {
         w.h = static_cast<int>(off) / pair;
         w.tile = static_cast<int>(off) - w.h * pair;
@@ -331,11 +332,22 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
         w.h = static_cast<int>(off / pair);
         w.tile = static_cast<int>(off % pair);
     }
+    if (PAIR > 0) {
+        // units ahead of the first tile belong to no tile
+        w.tile -= PAIR;
+        if (w.tile < 0) {
+            r.at -= w.tile;
+            w.tile = 0;
+        }
+    }
     if (ROWS > 32 && w.t.cost == 2) {
         // a tile belongs to the CTA that its first unit falls to
         r.at += w.tile & 1;
         w.tile = (w.tile + 1) >> 1;
-        if (w.tile == w.t.tiles && r.at < r.end) next_pair<ROWS, TILE>(a, w);
+        if (w.tile == w.t.tiles && r.at < r.end) {
+            next_pair<ROWS, TILE>(a, w);
+            r.at += PAIR;
+        }
     }
     return r;
 }
