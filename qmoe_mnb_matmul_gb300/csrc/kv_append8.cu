@@ -19,7 +19,8 @@
 // at once.  A warp (several for long blocks) takes a block of one head of keys or
 // values, a lane eight elements of a row as two runs of four that a rotation pairs, and
 // holds the warp's tokens in 64 registers between the largest value and the rounding.
-// Queries have CTAs of their own behind the units'.
+// Queries have CTAs of their own behind the units' (a launch of their own, with twice the
+// warps on an SM, made prompts of 16920 tokens 92 us instead of 83).
 //
 // Bound: HBM for prompts, three dependent loads for one token.
 #include <algorithm>
@@ -33,7 +34,10 @@ namespace mnb {
 
 namespace {
 
-constexpr int kHeldSteps = 8;  // steps of 32 / G tokens that a warp holds
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+// Steps of 32 / G tokens that a warp holds: 16, 8 or 8 tokens (G = 8, 16, 32), so that 16
+// warps hold a block of 128.
+constexpr int held_steps(int g) { return g == 32 ? 8 : 4; }
 
 __device__ __forceinline__ float smallest_scale(float largest) {
     const uint32_t bits = __float_as_uint(largest);
@@ -56,37 +60,36 @@ __device__ __forceinline__ float2 values2(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Division by a scale: exact by its reciprocal where it is a power of two (those that
-// this file makes), else a division.
-struct Divide {
-    float scale, inv;
-    bool power;
-    __device__ __forceinline__ explicit Divide(float s) {
-        scale = s;
-        inv = 1.f / s;
-        power = (__float_as_uint(s) & 0x7FFFFFu) == 0 && s >= 1.17549435e-38f;
-    }
-    __device__ __forceinline__ float operator()(float x) const { return power ? x * inv : __fdiv_rn(x, scale); }
-};
-
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// Four codes of x / scale, by the reciprocal where that is exact (the scales made here are powers of
+// two).  0 where the scale is 0; what is not finite becomes NaN (t + 0 t is t or NaN).
+template <bool EXACT>
+__device__ __forceinline__ uint32_t quotients4(const float (&x)[4], float scale, float inv) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = EXACT ? x[i] * inv : __fdiv_rn(x[i], scale);
+        t[i] = fmaf(t[i], 0.f, t[i]);
+    }
+    return codes4(t[0], t[1], t[2], t[3]);
+}
 
 // One block of one head, by the `wpb` warps from this one's `part` = 0 on: rows [from,
 // to) of the page are new, [begin, from) older.  src: the lane's head of the token in
-// row `from`; base: the page's head in the cache.  All warps of the CTA call it together
-// (`on`: this one has a block) where wpb > 1.
+// row `from`; page: looked at once the rows are on their way; angles: the new rows' in shared
+// memory, once `landed` has its copy.
 template <typename TI, int G, bool INTER>
-__device__ __forceinline__ void store_block(const KvAppendArgs& a, bool on, bool key, const TI* src, int64_t src_step,
-                                            uint8_t* base, float* scale_at, int begin, int from, int to, int64_t pos,
-                                            int part, int wpb, float* parts) {
-    constexpr int kPer = 32 / G;
-    const int lane = threadIdx.x & 31, sub = lane % G, group = lane / G, dim = a.cache.dim;
-    const bool in = on && sub * 8 < dim;
+__device__ __forceinline__ void store_block(const KvAppendArgs& a, bool key, int head, const TI* src, int64_t src_step, int page,
+                                            int begin, int from, int to, int part, int wpb, float* parts, const float* angles,
+                                            uint64_t* landed) {
+    constexpr int kPer = 32 / G, kHeldSteps = held_steps(G);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % G, group = lane / G, dim = a.cache.dim;
+    const bool in = sub * 8 < dim;
     const int half = key && a.cos_sin ? a.rot_dim / 2 : 0;
     const bool turns = sub * 4 < half, apart = turns && !INTER;
     const int i0 = apart ? sub * 4 : sub * 8, i1 = apart ? half + sub * 4 : sub * 8 + 4;
     const bool norm = key && a.k_norm != nullptr;
-    const float old = on && from > begin ? *scale_at : 0.f;
     const int row0 = begin + part * kHeldSteps * kPer + group;  // the lane's first row
     Raw4<TI> x[kHeldSteps], y[kHeldSteps];
 #pragma unroll
@@ -101,11 +104,17 @@ __device__ __forceinline__ void store_block(const KvAppendArgs& a, bool on, bool
             y[s] = {};
         }
     }
+    if (page < 0 || page >= a.cache.num_pages) return;  // (every warp of the CTA)
+    uint8_t* base = static_cast<uint8_t*>(key ? a.cache.k : a.cache.v) + page * a.cache.page_stride + head * a.cache.head_stride;
+    float* scale_at = (key ? a.cache.k_scale : a.cache.v_scale) + page * a.cache.scale_page_stride +
+                      head * a.cache.scale_head_stride + (begin >> a.cache.block_shift);
+    const float old = from > begin ? *scale_at : 0.f;
     Run4 wu = {{1.f, 1.f, 1.f, 1.f}}, ww = wu;
     if (norm && in) {
         wu = load4(a.k_norm + i0);
         ww = load4(a.k_norm + i1);
     }
+    if (half > 0) mbar_wait(landed, 0);
     float largest = 0.f;
     Run4 u[kHeldSteps], w[kHeldSteps];
 #pragma unroll
@@ -126,8 +135,9 @@ __device__ __forceinline__ void store_block(const KvAppendArgs& a, bool on, bool
             }
         }
         if (turns && in && row >= from && row < to) {
-            const float* angles = a.cos_sin + (pos + row - from) * a.rot_dim + sub * 4;
-            const Run4 cs = load4(angles), sn = load4(angles + half);
+            const float* turn = angles + (row - from) * a.rot_dim + sub * 4;
+            const float4 c4 = *reinterpret_cast<const float4*>(turn), s4 = *reinterpret_cast<const float4*>(turn + half);
+            const Run4 cs = {{c4.x, c4.y, c4.z, c4.w}}, sn = {{s4.x, s4.y, s4.z, s4.w}};
             if (INTER) {  // pairs (0, 1), (2, 3) of each run
                 const Run4 p = e, q = f;
                 e = {{fmaf(p.x[0], cs.x[0], -p.x[1] * sn.x[0]), fmaf(p.x[1], cs.x[0], p.x[0] * sn.x[0]),
@@ -146,37 +156,47 @@ __device__ __forceinline__ void store_block(const KvAppendArgs& a, bool on, bool
         u[s] = e;
         w[s] = f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (finite(e.x[i])) largest = fmaxf(largest, fabsf(e.x[i]));
-            if (finite(f.x[i])) largest = fmaxf(largest, fabsf(f.x[i]));
-        }
+        for (int i = 0; i < 4; ++i) largest = fmaxf(largest, fmaxf(fabsf(e.x[i]), fabsf(f.x[i])));  // (drops a NaN)
+    }
+    if (largest > 3.402823466e38f) {  // an infinity among them: the largest of the others
+        largest = 0.f;
+#pragma unroll
+        for (int s = 0; s < kHeldSteps; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (finite(u[s].x[i])) largest = fmaxf(largest, fabsf(u[s].x[i]));
+                if (finite(w[s].x[i])) largest = fmaxf(largest, fabsf(w[s].x[i]));
+            }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
-    if (wpb > 1) {
-        const int first = (threadIdx.x >> 5) - part;
-        if (lane == 0) parts[threadIdx.x >> 5] = largest;
-        __syncthreads();
+    if (wpb > 1) {  // (a named barrier of the block's warps; `parts` is another array in the next call)
+        const int first = warp - part;
+        if (lane == 0) parts[warp] = largest;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + first / wpb), "r"(wpb * 32) : "memory");
         for (int k = 0; k < wpb; ++k) largest = fmaxf(largest, parts[first + k]);
     }
-    if (!on) return;
     const float need = smallest_scale(largest);
     const float scale = need > old ? need : old;
-    const Divide by(scale);
-    // a value that is not finite, as NaN
-    auto quotient = [&](float v) { return !finite(v) ? __uint_as_float(0x7fffffffu) : scale == 0.f ? 0.f : by(v); };
+    const float inv = scale > 0.f ? 1.f / scale : 0.f;
+    const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0 && (scale == 0.f || scale >= 1.17549435e-38f);
+    auto store = [&](auto by_reciprocal) {
+        constexpr bool EXACT = decltype(by_reciprocal)::value;
 #pragma unroll
-    for (int s = 0; s < kHeldSteps; ++s) {
-        const int row = row0 + s * kPer;
-        if (!in || row < from || row >= to) continue;
-        uint8_t* dst = base + row * a.cache.token_stride;
-        *reinterpret_cast<uint32_t*>(dst + i0) =
-            codes4(quotient(u[s].x[0]), quotient(u[s].x[1]), quotient(u[s].x[2]), quotient(u[s].x[3]));
-        *reinterpret_cast<uint32_t*>(dst + i1) =
-            codes4(quotient(w[s].x[0]), quotient(w[s].x[1]), quotient(w[s].x[2]), quotient(w[s].x[3]));
-    }
+        for (int s = 0; s < kHeldSteps; ++s) {
+            const int row = row0 + s * kPer;
+            if (!in || row < from || row >= to) continue;
+            uint8_t* dst = base + row * a.cache.token_stride;
+            *reinterpret_cast<uint32_t*>(dst + i0) = quotients4<EXACT>(u[s].x, scale, inv);
+            *reinterpret_cast<uint32_t*>(dst + i1) = quotients4<EXACT>(w[s].x, scale, inv);
+        }
+    };
+    if (exact)
+        store(std::true_type{});
+    else
+        store(std::false_type{});
     if (scale > old && from > begin) {
-        const float ratio = by(old);
+        const float ratio = old * inv;  // (a scale that grew is a power of two)
 #pragma unroll 2
         for (int row = row0; row < min(from, begin + (part + 1) * kHeldSteps * kPer); row += kPer) {
             if (!in) continue;
@@ -192,11 +212,18 @@ __device__ __forceinline__ void store_block(const KvAppendArgs& a, bool on, bool
 
 // First kv_ctas CTAs: unit blockIdx.x / shares, a share of its heads of keys and values.
 // The others: a token per warp and a share of `steps` steps of its query heads.
-template <typename TI, int G, bool INTER, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append8_kernel(const KvAppendArgs a, int kv_ctas, int shares,
-                                                                          int q_shares, int steps) {
-    constexpr int kPer = 32 / G, kWarps = THREADS / 32;
+template <typename TI, int G, bool INTER>
+__global__ void __launch_bounds__(kThreads, G == 32 ? 1 : 2) kv_append8_kernel(const KvAppendArgs a, int kv_ctas, int shares, int q_shares,
+                                                                int steps) {
+    constexpr int kPer = 32 / G;
+    extern __shared__ __align__(16) float block_angles[];
     __shared__ float parts[2][kWarps];
+    __shared__ __align__(8) uint64_t landed;
+    if (threadIdx.x == 0) {
+        mbar_init(&landed, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = a.cache.dim;
@@ -204,23 +231,35 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append8_kernel(cons
     const KvStep& st = a.step;
     if (static_cast<int>(blockIdx.x) < kv_ctas) {
         const int unit = blockIdx.x / shares, share = blockIdx.x % shares;
-        int b = unit, k = 0;
+        int b = unit, k = 0, first = unit, count = 1;
+        int64_t len = 0;
         if (st.new_start) {
             // the sequence that the unit's number falls to: the last with new_start / rows + 2 b at most that
-            int upto = 0;
+            unsigned found = 0;
             for (int b0 = 0; b0 < st.batch; b0 += 32) {
                 const int s = b0 + lane;
-                const bool at_most = s < st.batch && (max(__ldg(st.new_start + s), 0) >> shift) + 2 * s <= unit;
-                upto += __popc(__ballot_sync(0xffffffffu, at_most));
+                const bool is = s < st.batch;
+                const int lo = is ? __ldg(st.new_start + s) : 0, hi = is ? __ldg(st.new_start + s + 1) : 0;
+                const int n = is ? __ldg(st.seq_lens + s) : 0;
+                const unsigned at_most = __ballot_sync(0xffffffffu, is && (max(lo, 0) >> shift) + 2 * s <= unit);
+                if (at_most == 0) break;
+                found = at_most;
+                const int src = __popc(at_most) - 1;
+                b = b0 + src;
+                first = __shfl_sync(0xffffffffu, lo, src);
+                count = __shfl_sync(0xffffffffu, hi, src);
+                len = __shfl_sync(0xffffffffu, n, src);
+                if (at_most != 0xffffffffu) break;
             }
-            b = upto - 1;
-            if (b < 0) return;
-            k = unit - (max(__ldg(st.new_start + b), 0) >> shift) - 2 * b;
+            if (found == 0) return;
+            k = unit - (max(first, 0) >> shift) - 2 * b;
+            first = min(max(first, 0), st.tokens);
+            count = max(min(max(count, 0), st.tokens) - first, 0);
+        } else {
+            len = __ldg(st.seq_lens + b);
         }
-        int first, count;
-        step_tokens(st, b, &first, &count);
         // tokens [skip, count) have positions from pos0 on
-        const int64_t len = __ldg(st.seq_lens + b), before = len - count;
+        const int64_t before = len - count;
         const int skip = static_cast<int>(before < 0 ? -before : 0);
         const int64_t pos0 = before < 0 ? 0 : before;
         if (skip >= count || k < 0) return;
@@ -235,27 +274,34 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append8_kernel(cons
         }
         int page = -1;
         if (lo < st.capacity) page = __ldg(st.page_table + b * st.table_stride + lo / a.cache.page_size);
-        if (page < 0 || page >= a.cache.num_pages) bad = true;
-        if (bad && threadIdx.x == 0) record_error(MNB_ERR_CONTENT);
-        if (lo >= hi || page < 0 || page >= a.cache.num_pages) return;
+        if (lo >= hi) {
+            if (threadIdx.x == 0) record_error(MNB_ERR_CONTENT);
+            return;
+        }
         const int begin = static_cast<int>((block << shift) % a.cache.page_size);
         const int from = begin + static_cast<int>(lo - (block << shift)), to = from + static_cast<int>(hi - lo);
         const int64_t token = first + skip + (lo - pos0);
-        const int wpb = max(1, rows / (kHeldSteps * kPer)), slots = kWarps / wpb;
+        const int wpb = max(1, rows / (held_steps(G) * kPer)), slots = kWarps / wpb;
+        // the new rows' angles, where this CTA has keys (positions are neighbours in the table)
+        const bool turned = a.cos_sin && share * slots < a.cache.heads;
+        if (turned && threadIdx.x == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(hi - lo) * a.rot_dim * 4;
+            mbar_arrive_expect_tx(&landed, bytes);
+            bulk_g2s(block_angles, a.cos_sin + lo * a.rot_dim, bytes, &landed);
+        }
         const int slot = warp / wpb, part = warp % wpb, jobs = 2 * a.cache.heads;
         int pass = 0;
         for (int j0 = share * slots; j0 < jobs; j0 += shares * slots, pass ^= 1) {
             const int job = j0 + slot, head = job < a.cache.heads ? job : job - a.cache.heads;
-            const bool on = job < jobs, key = job < a.cache.heads;
-            if (!on && wpb == 1) break;
+            const bool key = job < a.cache.heads;
+            if (job >= jobs) break;  // (with it the other warps of its block)
             const TI* src = static_cast<const TI*>(key ? a.k : a.v) + token * (key ? a.k_stride : a.v_stride) + int64_t(head) * dim;
-            uint8_t* base = static_cast<uint8_t*>(key ? a.cache.k : a.cache.v) + page * a.cache.page_stride +
-                            head * a.cache.head_stride;
-            float* scale = (key ? a.cache.k_scale : a.cache.v_scale) + page * a.cache.scale_page_stride +
-                           head * a.cache.scale_head_stride + (begin >> shift);
-            store_block<TI, G, INTER>(a, on, key, src, key ? a.k_stride : a.v_stride, base, scale, begin, from, to, lo, part,
-                                      wpb, parts[pass]);
+            store_block<TI, G, INTER>(a, key, head, src, key ? a.k_stride : a.v_stride, page, begin, from, to, part, wpb,
+                                      parts[pass], block_angles, &landed);
         }
+        if (page < 0 || page >= a.cache.num_pages) bad = true;
+        if (bad && threadIdx.x == 0) record_error(MNB_ERR_CONTENT);
+        if (turned && threadIdx.x == 0) mbar_wait(&landed, 0);  // no copy may be in flight when the CTA ends
         return;
     }
     // ---- queries
@@ -291,15 +337,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append8_kernel(cons
 
 template <typename TI, int G, bool INTER>
 cudaError_t launch_pairs(const KvAppendArgs& a, int sm_count, bool pdl, cudaStream_t stream) {
-    // blocks of up to 128 rows: eight tokens of 256 elements a warp need 16 warps
-    constexpr int THREADS = G == 32 ? 512 : 256, kWarps = THREADS / 32, kPer = 32 / G;
+    constexpr int kPer = 32 / G;
     const int rows = 1 << a.cache.block_shift;
-    const int slots = kWarps / std::max(1, rows / (kHeldSteps * kPer));
+    const int slots = kWarps / std::max(1, rows / (held_steps(G) * kPer));
     const int64_t units = a.step.new_start ? a.step.tokens / rows + int64_t(2) * a.step.batch : a.step.batch;
-    // a block's heads are shared by as many CTAs as give every SM about eight: few blocks
+    // a block's heads are shared by as many CTAs as give every SM about four: few blocks
     // are bound by latency
     const int most = cdiv(2 * a.cache.heads, slots);
-    const int shares = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(sm_count) * 8 / units)));
+    const int shares = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(sm_count) * 4 / units)));
     const int64_t kv_ctas = units * shares;
     int64_t q_ctas = 0;
     int q_shares = 1, steps = 1;
@@ -311,9 +356,10 @@ cudaError_t launch_pairs(const KvAppendArgs& a, int sm_count, bool pdl, cudaStre
         q_ctas = cdiv<int64_t>(a.step.tokens, kWarps) * q_shares;
     }
     if (kv_ctas + q_ctas > 0x7fffffff) return cudaErrorNotSupported;
-    return launch_ready<kv_append8_kernel<TI, G, INTER, THREADS>>(dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(THREADS),
-                                                                  0, stream, pdl, a, static_cast<int>(kv_ctas), shares,
-                                                                  q_shares, steps);
+    const size_t smem = a.cos_sin ? size_t(rows) * a.rot_dim * 4 : 0;
+    return launch_cluster<kv_append8_kernel<TI, G, INTER>>(dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(kThreads), 1, smem,
+                                                           128 * 256 * 4, stream, pdl, a, static_cast<int>(kv_ctas), shares,
+                                                           q_shares, steps);
 }
 
 template <typename TI, int G>
