@@ -24,9 +24,11 @@ MNB_SLICE_DECL(kv_attention_bf16_qf32)
                      int sm_count, bool pdl, cudaStream_t stream, int* ctas);                                   \
     cudaError_t NAME##_take_error(unsigned int* out);
 MNB_SLICE_DECL(kv_attention8_q16_64)
+MNB_SLICE_DECL(kv_attention8_q16_96)
 MNB_SLICE_DECL(kv_attention8_q16_128)
 MNB_SLICE_DECL(kv_attention8_q16_256)
 MNB_SLICE_DECL(kv_attention8_qf32_64)
+MNB_SLICE_DECL(kv_attention8_qf32_96)
 MNB_SLICE_DECL(kv_attention8_qf32_128)
 MNB_SLICE_DECL(kv_attention8_qf32_256)
 #undef MNB_SLICE_DECL
@@ -233,7 +235,8 @@ cudaError_t kv_attention_take_error(unsigned int* out) {
                       kv_attention_bf16_qf32_take_error, kv_attention8_q16_64_take_error,
                       kv_attention8_q16_128_take_error, kv_attention8_q16_256_take_error,
                       kv_attention8_qf32_64_take_error, kv_attention8_qf32_128_take_error,
-                      kv_attention8_qf32_256_take_error}) {
+                      kv_attention8_qf32_256_take_error, kv_attention8_q16_96_take_error,
+                      kv_attention8_qf32_96_take_error}) {
         unsigned int v = 0;
         const cudaError_t e = take(&v);
         if (e != cudaSuccess) return e;
@@ -266,9 +269,10 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     const bool bf = a.cache.dtype == kBF16, f32 = q_dtype == kF32;
     int ctas = 0;
     if (codes) {
-        auto slice = pad == 64    ? (f32 ? kv_attention8_qf32_64 : kv_attention8_q16_64)
-                     : pad == 128 ? (f32 ? kv_attention8_qf32_128 : kv_attention8_q16_128)
-                                  : (f32 ? kv_attention8_qf32_256 : kv_attention8_q16_256);
+        auto slice = pad == 64             ? (f32 ? kv_attention8_qf32_64 : kv_attention8_q16_64)
+                     : a.cache.dim <= 96 ? (f32 ? kv_attention8_qf32_96 : kv_attention8_q16_96)
+                     : pad == 128        ? (f32 ? kv_attention8_qf32_128 : kv_attention8_q16_128)
+                                         : (f32 ? kv_attention8_qf32_256 : kv_attention8_q16_256);
         e = slice(kmap, vmap, a, rows, sm_count, pdl, stream, &ctas);
     } else {
         auto slice = bf ? (f32 ? kv_attention_bf16_qf32 : kv_attention_bf16) : (f32 ? kv_attention_f16_qf32 : kv_attention_f16);

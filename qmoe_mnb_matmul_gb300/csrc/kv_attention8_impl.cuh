@@ -44,6 +44,7 @@ namespace {
 template <int DP, int ROWS, bool QF32>
 struct Plan8 {
     static constexpr int kParts = QF32 ? 2 : 1;  // fp16 parts of a query
+    static constexpr int kPad = DP <= 64 ? 64 : DP <= 128 ? 128 : 256;  // of the split parts' rows
     static constexpr int kTile = kv_tile8(ROWS, DP);
     static constexpr int kPanels = (DP + 127) / 128;  // of 128 columns (the last may be padding)
     static constexpr int kSlotBytes = kTile * kPanels * 128;
@@ -64,10 +65,18 @@ struct Plan8 {
     static_assert(kSlots >= 2, "a key tile and a value tile must fit");
 };
 
-// What a pair costs besides its tiles, in tiles: its queries, the first tile's way, the
-// join of the warps, the store (64 sequences of 1 .. 8192 tokens: 136 us with none, 117
-// with one, 107 with two, 99 with three, 97 with four; 8 of 2000: 15.0 with three, 15.5 with four).
-constexpr int kPairUnits = 3;
+// What a pair costs besides its tiles (its queries, the first tile's way, the join of the
+// warps, the store), in tiles: 64 sequences of 1 .. 8192 tokens 136 us with none, 117 with
+// one, 107 with two, 99 with three, 97 with four; 8 of 2000 tokens 15.0 with three, 15.5 with four.
+// With more rows a tile's cost grows with them (of 64 tokens: 4 units up to 8 rows, 12 for 33 and
+// more): 16 sequences of 4 .. 20 rows, heads of 80, 50 us with one unit for all, 42 with these.
+template <int ROWS>
+struct Costs8 {
+    static constexpr int kMost = ROWS == 8 ? 1 : ROWS == 32 ? 7 : 12, kPair = ROWS == 8 ? 3 : 16;
+    static __device__ __forceinline__ int of(int rows) {
+        return ROWS == 8 ? 1 : rows <= 8 ? 4 : rows <= 16 ? 5 : rows <= 32 ? 7 : 12;
+    }
+};
 
 // Two codes (the low 16 bits) as fp16.
 __device__ __forceinline__ uint32_t halves(uint32_t codes) {
@@ -140,7 +149,7 @@ __device__ __forceinline__ void produce8(const KvAttnArgs& a, const CUtensorMap*
     int64_t at = r.at;
     bool ok = true, bad = false;
     while (at < r.end && ok) {
-        const int nt = part_tiles<ROWS>(w, r.end - at);
+        const int nt = part_tiles<Costs8<ROWS>>(w, r.end - at);
         bad = bad || w.pos0 + w.count > a.step.capacity;
         const int first = (w.t.lo / TILE + w.tile) * TILE;
         Cursor box, mine;  // of the boxes, and of the scales (two tiles ahead)
@@ -195,8 +204,8 @@ __device__ __forceinline__ void produce8(const KvAttnArgs& a, const CUtensorMap*
         at += nt * w.t.cost;
         w.tile += nt;
         if (at < r.end) {
-            next_pair<ROWS, TILE>(a, w);
-            at += kPairUnits;
+            next_pair<ROWS, TILE, Costs8<ROWS>>(a, w);
+            at += Costs8<ROWS>::kPair;
         }
     }
     // a page number outside the cache: its tokens read as zeros; or a length past the page table
@@ -727,7 +736,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                             kv_log_sum(ml.x, ml.y, kShift);
                 } else {
                     const int64_t at = static_cast<int64_t>(part) * ROWS + rr;
-                    *reinterpret_cast<float4*>(a.part_o + at * DP + d) = sum;
+                    *reinterpret_cast<float4*>(a.part_o + at * P::kPad + d) = sum;
                     if (d == 0) a.part_ml[at] = ml;
                 }
             }
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
     grid_launch_dependents();
 
     Walk w = {};
-    const Range r = find_range<ROWS, TILE, kPairUnits>(a, w);
+    const Range r = find_range<ROWS, TILE, Costs8<ROWS>>(a, w);
     if (warp == kComputeWarps) {
         produce8<DP, ROWS, QF32, KSLOTS, true>(a, &kmap, sm.k, scales, k_full, k_empty, w, r);
         return;
@@ -795,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
     int4 join = make_int4(-1, 0, 0, 0);
 #pragma unroll 1
     while (at < r.end) {
-        const int nt = part_tiles<ROWS>(w, r.end - at);
+        const int nt = part_tiles<Costs8<ROWS>>(w, r.end - at);
         const bool whole = w.tile == 0 && nt == w.t.tiles;
         const int slot = at == r.at ? 0 : 1, part = 2 * blockIdx.x + slot;  // (r.at is the first part's first unit)
         // the warps split along the rows only as far as the pair's rows need
@@ -821,8 +830,8 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
         at += nt * w.t.cost;
         w.tile += nt;
         if (at < r.end) {
-            next_pair<ROWS, TILE>(a, w);
-            at += kPairUnits;
+            next_pair<ROWS, TILE, Costs8<ROWS>>(a, w);
+            at += Costs8<ROWS>::kPair;
         }
     }
     if (warp == 0 && lane == 0) a.join[blockIdx.x] = join;

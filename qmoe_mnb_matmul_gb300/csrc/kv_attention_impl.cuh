@@ -127,7 +127,7 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
     int64_t at = r.at;
     bool ok = true, bad = false;
     while (at < r.end && ok) {
-        const int nt = part_tiles<ROWS>(w, r.end - at);
+        const int nt = part_tiles<Costs16<ROWS>>(w, r.end - at);
         bad = bad || w.pos0 + w.count > a.step.capacity;
         int tok = (w.t.lo / kKvTile + w.tile) * kKvTile + row0;
         // page and row of the box at token tok; boxes that no row sees are asked for
@@ -159,7 +159,7 @@ __device__ __forceinline__ void produce(const KvAttnArgs& a, const CUtensorMap* 
         }
         at += nt * w.t.cost;
         w.tile += nt;
-        if (at < r.end) next_pair<ROWS, kKvTile>(a, w);
+        if (at < r.end) next_pair<ROWS, kKvTile, Costs16<ROWS>>(a, w);
     }
     // a page number outside the cache: its tokens read as zeros; or a length past the page table
     if (bad) record_error(MNB_ERR_CONTENT);
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
     grid_launch_dependents();
 
     Walk w = {};
-    const Range r = find_range<ROWS, kKvTile>(a, w);
+    const Range r = find_range<ROWS, kKvTile, Costs16<ROWS>>(a, w);
     if (warp == kComputeWarps) {
         produce<DP, ROWS, KSLOTS>(a, &kmap, sm.k, k_full, k_empty, w, r);
         return;
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
     int4 join = make_int4(-1, 0, 0, 0);
 #pragma unroll 1
     while (at < r.end) {
-        const int nt = part_tiles<ROWS>(w, r.end - at);
+        const int nt = part_tiles<Costs16<ROWS>>(w, r.end - at);
         const bool whole = w.tile == 0 && nt == w.t.tiles;
         const int slot = at == r.at ? 0 : 1, part = 2 * blockIdx.x + slot;  // (r.at is the first part's first unit)
         // the warps split along the rows only as far as the pair's rows need
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, Plan<DP, ROWS, QF32, query_parts(DT,
         }
         at += nt * w.t.cost;
         w.tile += nt;
-        if (at < r.end) next_pair<ROWS, kKvTile>(a, w);
+        if (at < r.end) next_pair<ROWS, kKvTile, Costs16<ROWS>>(a, w);
     }
     if (warp == 0 && lane == 0) a.join[blockIdx.x] = join;
 }

@@ -145,6 +145,15 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
 
 // ------------------------------------------------------------- the units
 
+// What the tiles of a pair cost, in units: of(rows in use), at most kMost, and kPair for the
+// pair itself.  Over a 16-bit cache: a tile of more than 32 rows takes about twice the time
+// of one that HBM bounds (its matrix instructions bound it: measured 4900 against 2700 cycles).
+template <int ROWS>
+struct Costs16 {
+    static constexpr int kMost = ROWS > 32 ? 2 : 1, kPair = 0;
+    static __device__ __forceinline__ int of(int rows) { return ROWS > 32 && rows > 32 ? 2 : 1; }
+};
+
 // A row tile of one sequence: what its rows may see.
 struct RowTile {
     int first_row;  // flat index (token * group + head) of the tile's first row
@@ -168,7 +177,7 @@ __device__ __forceinline__ int window_start(const KvAttnArgs& a, int pos) {
     return a.window > 0 && pos >= a.window ? min(pos + 1 - a.window, a.step.capacity) : 0;
 }
 
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, typename COSTS>
 __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int pos0, int rt) {
     RowTile t;
     const int all = count * a.group;
@@ -180,9 +189,7 @@ __device__ __forceinline__ RowTile row_tile(const KvAttnArgs& a, int count, int 
     t.hi_all = min(max(pos0 + tok0 + 1, 0), cap);
     t.lo = window_start(a, pos0 + tok0);
     t.lo_all = window_start(a, pos0 + tok1);
-    // a tile of more than 32 rows takes about twice the time of one that HBM bounds
-    // (its matrix instructions bound it: measured 4900 against 2700 cycles)
-    t.cost = ROWS > 32 && t.rows > 32 ? 2 : 1;
+    t.cost = COSTS::of(t.rows);
     t.tiles = t.hi > t.lo ? (t.hi + TILE - 1) / TILE - t.lo / TILE : 1;
     return t;
 }
@@ -200,20 +207,20 @@ __device__ __forceinline__ void load_sequence(const KvAttnArgs& a, Walk& w, int 
 }
 
 // Units of the sequence in w over all its row tiles, for one key-value head: those of its
-// tiles, and PAIR more ahead of each row tile's for what a pair costs by itself.
-template <int ROWS, int TILE, int PAIR>
+// tiles, and COSTS::kPair more ahead of each row tile's for what a pair costs by itself.
+template <int ROWS, int TILE, typename COSTS>
 __device__ __forceinline__ int64_t sequence_units(const KvAttnArgs& a, const Walk& w) {
     int64_t n = 0;
 #pragma unroll 1
     for (int rt = 0; rt < w.row_tiles; ++rt) {
-        const RowTile t = row_tile<ROWS, TILE>(a, w.count, w.pos0, rt);
-        n += t.tiles * t.cost + PAIR;
+        const RowTile t = row_tile<ROWS, TILE, COSTS>(a, w.count, w.pos0, rt);
+        n += t.tiles * t.cost + COSTS::kPair;
     }
     return n;
 }
 
 // The next pair after a finished one (call only while units remain).
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, typename COSTS>
 __device__ __forceinline__ void next_pair(const KvAttnArgs& a, Walk& w) {
     w.tile = 0;
     if (++w.h < a.cache.heads) return;
@@ -225,7 +232,7 @@ __device__ __forceinline__ void next_pair(const KvAttnArgs& a, Walk& w) {
         } while (w.row_tiles == 0);
         w.rt = 0;
     }
-    w.t = row_tile<ROWS, TILE>(a, w.count, w.pos0, w.rt);
+    w.t = row_tile<ROWS, TILE, COSTS>(a, w.count, w.pos0, w.rt);
 }
 
 // The CTA's range of units.  CTA c of the `ctas` that have units takes `each` of them,
@@ -263,7 +270,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {
 // the range begins in again.  The way from the launch to the first copy passes
 // through here, so it is short rather than general: with up to 32 sequences one load
 // of lengths, two 32-bit divisions (one of the units, one of the pair).
-template <int ROWS, int TILE, int PAIR = 0>
+template <int ROWS, int TILE, typename COSTS>
 __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     const int lane = threadIdx.x & 31, batch = a.step.batch, per = (batch + 31) / 32;
     const int64_t heads = a.cache.heads;
@@ -272,7 +279,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
 #pragma unroll 4
     for (int s = lane * per; s < min((lane + 1) * per, batch); ++s) {
         load_sequence<ROWS>(a, mine, s);
-        units += sequence_units<ROWS, TILE, PAIR>(a, mine);
+        units += sequence_units<ROWS, TILE, COSTS>(a, mine);
     }
     units *= heads;
     int64_t incl = warp_scan(units);
@@ -281,7 +288,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     r.at = r.end = r.each = 0;
     r.more = 0;
     // a range holds a tile's first unit: as many units as the dearest tile has
-    r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total / (ROWS > 32 ? 2 : 1)));
+    r.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total / COSTS::kMost));
     if (total > 0 && r.ctas == 0) r.ctas = 1;
     const int c = blockIdx.x;
     if (c >= r.ctas) return r;  // fewer units than CTAs
@@ -299,7 +306,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
             units = 0;
             if (s0 + lane < last) {
                 load_sequence<ROWS>(a, mine, s0 + lane);
-                units = sequence_units<ROWS, TILE, PAIR>(a, mine) * heads;
+                units = sequence_units<ROWS, TILE, COSTS>(a, mine) * heads;
             }
             incl = before + warp_scan(units);
             begin = incl - units;
@@ -319,12 +326,12 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     int64_t off = r.at - __shfl_sync(0xffffffffu, begin, src);
 #pragma unroll 1
     for (w.rt = 0;; ++w.rt) {
-        w.t = row_tile<ROWS, TILE>(a, w.count, w.pos0, w.rt);
-        const int64_t n = (static_cast<int64_t>(w.t.tiles) * w.t.cost + PAIR) * heads;
+        w.t = row_tile<ROWS, TILE, COSTS>(a, w.count, w.pos0, w.rt);
+        const int64_t n = (static_cast<int64_t>(w.t.tiles) * w.t.cost + COSTS::kPair) * heads;
         if (off < n) break;
         off -= n;
     }
-    const int pair = w.t.tiles * w.t.cost + PAIR;  // units of a pair: below 2^28
+    const int pair = w.t.tiles * w.t.cost + COSTS::kPair;  // units of a pair: below 2^31
     if (off < (int64_t(1) << 31)) {
         w.h = static_cast<int>(off) / pair;
         w.tile = static_cast<int>(off) - w.h * pair;
@@ -332,30 +339,35 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
         w.h = static_cast<int>(off / pair);
         w.tile = static_cast<int>(off % pair);
     }
-    if (PAIR > 0) {
+    if (COSTS::kPair > 0) {
         // units ahead of the first tile belong to no tile
-        w.tile -= PAIR;
+        w.tile -= COSTS::kPair;
         if (w.tile < 0) {
             r.at -= w.tile;
             w.tile = 0;
         }
     }
-    if (ROWS > 32 && w.t.cost == 2) {
-        // a tile belongs to the CTA that its first unit falls to
-        r.at += w.tile & 1;
-        w.tile = (w.tile + 1) >> 1;
+    if (COSTS::kMost > 1) {
+        // (w.tile counts units) a tile belongs to the CTA that its first unit falls to
+        const int unit = w.tile, cost = w.t.cost;
+        w.tile = (unit + cost - 1) / cost;
+        r.at += w.tile * cost - unit;
         if (w.tile == w.t.tiles && r.at < r.end) {
-            next_pair<ROWS, TILE>(a, w);
-            r.at += PAIR;
+            next_pair<ROWS, TILE, COSTS>(a, w);
+            r.at += COSTS::kPair;
         }
     }
     return r;
 }
 
 // Tiles of the walk's pair that begin within the next `units`.
-template <int ROWS>
+template <typename COSTS>
 __device__ __forceinline__ int part_tiles(const Walk& w, int64_t units) {
-    if (ROWS > 32 && w.t.cost == 2) units = (units + 1) >> 1;
+    if (COSTS::kMost > 1) {
+        // (units past the pair's end do not matter: a division in 32 bits)
+        const int some = static_cast<int>(min(units, static_cast<int64_t>(0x7fffffff - COSTS::kMost)));
+        units = (some + w.t.cost - 1) / w.t.cost;
+    }
     return static_cast<int>(min(static_cast<int64_t>(w.t.tiles - w.tile), units));
 }
 
