@@ -75,6 +75,42 @@ __device__ __forceinline__ uint32_t quotients4(const float (&x)[4], float scale,
     return codes4(t[0], t[1], t[2], t[3]);
 }
 
+// The last sequence whose first new token passes `upto` (which holds up to one sequence and for
+// none behind it), its first and last new token's end and its length; without new_start
+// sequence n itself, with one token.  128 sequences are asked for at a time, their lengths with
+// them: the way to a token's page is three loads long.
+struct Located {
+    int seq, start, end, len;
+};
+template <typename F>
+__device__ __forceinline__ Located locate(const KvStep& st, int n, F upto) {
+    if (st.new_start == nullptr) return {n, n, n + 1, __ldg(st.seq_lens + n)};
+    const int lane = threadIdx.x & 31;
+    Located r = {-1, 0, 0, 0};
+    for (int b0 = 0; b0 < st.batch; b0 += 128) {
+        int lo[4], hi[4], len[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = b0 + 32 * i + lane;
+            const bool is = s < st.batch;
+            lo[i] = is ? __ldg(st.new_start + s) : 0;
+            hi[i] = is ? __ldg(st.new_start + s + 1) : 0;
+            len[i] = is ? __ldg(st.seq_lens + s) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s0 = b0 + 32 * i;
+            const unsigned yes = __ballot_sync(0xffffffffu, s0 + lane < st.batch && upto(lo[i], s0 + lane));
+            if (yes == 0) return r;
+            const int src = __popc(yes) - 1;
+            r = {s0 + src, __shfl_sync(0xffffffffu, lo[i], src), __shfl_sync(0xffffffffu, hi[i], src),
+                 __shfl_sync(0xffffffffu, len[i], src)};
+            if (yes != 0xffffffffu) return r;
+        }
+    }
+    return r;
+}
+
 // One block of one head, by the `wpb` warps from this one's `part` = 0 on: rows [from,
 // to) of the page are new, [begin, from) older.  src: the lane's head of the token in
 // row `from`; page: looked at once the rows are on their way; angles: the new rows' in shared
@@ -231,33 +267,12 @@ __global__ void __launch_bounds__(kThreads, G == 32 ? 1 : 2) kv_append8_kernel(c
     const KvStep& st = a.step;
     if (static_cast<int>(blockIdx.x) < kv_ctas) {
         const int unit = blockIdx.x / shares, share = blockIdx.x % shares;
-        int b = unit, k = 0, first = unit, count = 1;
-        int64_t len = 0;
-        if (st.new_start) {
-            // the sequence that the unit's number falls to: the last with new_start / rows + 2 b at most that
-            unsigned found = 0;
-            for (int b0 = 0; b0 < st.batch; b0 += 32) {
-                const int s = b0 + lane;
-                const bool is = s < st.batch;
-                const int lo = is ? __ldg(st.new_start + s) : 0, hi = is ? __ldg(st.new_start + s + 1) : 0;
-                const int n = is ? __ldg(st.seq_lens + s) : 0;
-                const unsigned at_most = __ballot_sync(0xffffffffu, is && (max(lo, 0) >> shift) + 2 * s <= unit);
-                if (at_most == 0) break;
-                found = at_most;
-                const int src = __popc(at_most) - 1;
-                b = b0 + src;
-                first = __shfl_sync(0xffffffffu, lo, src);
-                count = __shfl_sync(0xffffffffu, hi, src);
-                len = __shfl_sync(0xffffffffu, n, src);
-                if (at_most != 0xffffffffu) break;
-            }
-            if (found == 0) return;
-            k = unit - (max(first, 0) >> shift) - 2 * b;
-            first = min(max(first, 0), st.tokens);
-            count = max(min(max(count, 0), st.tokens) - first, 0);
-        } else {
-            len = __ldg(st.seq_lens + b);
-        }
+        // the sequence that the unit's number falls to
+        const Located at = locate(st, unit, [&](int start, int s) { return (max(start, 0) >> shift) + 2 * s <= unit; });
+        if (at.seq < 0) return;
+        const int b = at.seq, k = st.new_start ? unit - (max(at.start, 0) >> shift) - 2 * b : 0;
+        const int first = min(max(at.start, 0), st.tokens), count = max(min(max(at.end, 0), st.tokens) - first, 0);
+        const int64_t len = at.len;
         // tokens [skip, count) have positions from pos0 on
         const int64_t before = len - count;
         const int skip = static_cast<int>(before < 0 ? -before : 0);
@@ -307,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, G == 32 ? 1 : 2) kv_append8_kernel(c
     // ---- queries
     const int index = blockIdx.x - kv_ctas, t = index / q_shares * kWarps + warp, q_share = index % q_shares;
     if (t >= st.tokens) return;
-    const int seq = sequence_of(st, t);
-    if (seq < 0) return;
-    int first, count;
-    step_tokens(st, seq, &first, &count);
-    const int64_t pos = int64_t(__ldg(st.seq_lens + seq)) - count + (t - first);
+    const Located of = locate(st, t, [&](int start, int) { return start <= t; });
+    const int seq = of.seq;
+    if (seq < 0 || (st.new_start && of.end <= t)) return;
+    const int first = min(max(of.start, 0), st.tokens), count = max(min(max(of.end, 0), st.tokens) - first, 0);
+    const int64_t pos = int64_t(of.len) - count + (t - first);
     if (pos < 0) return;
     const int sub = lane % G, group = lane / G;
     const bool in = sub * 8 < dim;

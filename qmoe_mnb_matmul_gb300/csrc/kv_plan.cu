@@ -27,6 +27,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;          // the largest cluster
+constexpr int kAtOnce = 4;               // pages that a thread looks for together
+constexpr int kSlotRun = 8;              // tokens of a thread in the slot map's own grid
 constexpr uint32_t kMost = 0x7fffffffu;  // sums stay there once they reach it
 
 // Sums of non-negative numbers that stop at kMost: the order does not matter.
@@ -176,11 +178,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanArgs 
         return a.page_table[b * a.table_stride + target[b] + (r - gives[b])];
     };
     auto popped = [&](uint32_t i) { return i < back ? given(i) : a.free_pages[room - 1 - i]; };
-    for (int64_t i = g0; i < taken; i += step) {
-        const uint32_t p = static_cast<uint32_t>(i);
-        const int b = last_at_most(takes, batch, p), page = popped(p);
-        if (page < 0 || page >= a.num_pages) bad = true;
-        a.page_table[b * a.table_stride + held[b] + (p - takes[b])] = page;
+    for (int64_t i = g0; i < taken; i += kAtOnce * step) {  // (several at a time: their loads do not wait for one another)
+        int b[kAtOnce], page[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t p = i + k * step;
+            if (p >= taken) break;
+            page[k] = popped(static_cast<uint32_t>(p));
+            b[k] = last_at_most(takes, batch, static_cast<uint32_t>(p));
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t p = i + k * step;
+            if (p >= taken) break;
+            if (page[k] < 0 || page[k] >= a.num_pages) bad = true;
+            a.page_table[b[k] * a.table_stride + held[b[k]] + (static_cast<uint32_t>(p) - takes[b[k]])] = page[k];
+        }
     }
     for (int64_t r = taken + g0; r < back; r += step) {
         const int64_t place = room - 1 - r;
@@ -203,19 +216,40 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanArgs 
     if (bad) record_error(MNB_ERR_CONTENT);
 }
 
-// The slot map of a large step, from the plan that the kernel ahead wrote.
+// The slot map of a large step, from the plan that the kernel ahead wrote: a warp takes 32
+// kSlotRun neighbouring tokens, finds the first one's sequence (the starts are in shared
+// memory) and goes on from there, a lane with every 32nd token.
 __global__ void __launch_bounds__(256) kv_slots_kernel(const KvPlanArgs a) {
+    extern __shared__ uint32_t starts[];
     grid_dependency_wait();
     grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tokens = a.new_start[a.batch];
+    if (static_cast<int64_t>(blockIdx.x) * 256 * kSlotRun >= tokens) return;
+    for (int b = threadIdx.x; b <= a.batch; b += 256) starts[b] = a.new_start[b];
+    __syncthreads();
     bool bad = false;
-    for (int t = blockIdx.x * 256 + threadIdx.x; t < tokens; t += gridDim.x * 256) {
-        const int b = last_at_most(reinterpret_cast<const uint32_t*>(a.new_start), a.batch, t);
-        const int pos = a.seq_lens[b] - a.new_start[b + 1] + t, column = a.by_page(pos);
-        const int page = a.page_table[b * a.table_stride + column];
-        const bool out = page < 0 || page >= a.num_pages;
-        if (out) bad = true;
-        a.slots[t] = out ? -1 : static_cast<int64_t>(page) * a.page_size + (pos - column * a.page_size);
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * 32 * kSlotRun; t0 < tokens;
+         t0 += static_cast<int64_t>(gridDim.x) * 256 * kSlotRun) {
+        int b = last_at_most(starts, a.batch, static_cast<uint32_t>(t0));
+        int page[kSlotRun], row[kSlotRun];
+#pragma unroll
+        for (int k = 0; k < kSlotRun; ++k) {
+            const int64_t t = t0 + 32 * k + lane;
+            if (t >= tokens) break;
+            while (starts[b + 1] <= static_cast<uint32_t>(t)) ++b;  // (ends: starts[batch] = tokens > t)
+            const int pos = a.seq_lens[b] - static_cast<int>(starts[b + 1]) + static_cast<int>(t), column = a.by_page(pos);
+            row[k] = pos - column * a.page_size;
+            page[k] = a.page_table[b * a.table_stride + column];
+        }
+#pragma unroll
+        for (int k = 0; k < kSlotRun; ++k) {
+            const int64_t t = t0 + 32 * k + lane;
+            if (t >= tokens) break;
+            const bool out = page[k] < 0 || page[k] >= a.num_pages;
+            if (out) bad = true;
+            a.slots[t] = out ? -1 : static_cast<int64_t>(page[k]) * a.page_size + row[k];
+        }
     }
     if (bad) record_error(MNB_ERR_CONTENT);
 }
@@ -239,8 +273,9 @@ cudaError_t launch_kv_plan(const KvPlanArgs& in, int sm_count, bool pdl, cudaStr
                                                          static_cast<unsigned>(ctas), smem,
                                                          size_t(7) * sizeof(uint32_t) * kKvPlanMaxBatch, stream, pdl, a, inside);
     if (e != cudaSuccess || !own_grid) return e;
-    const int grid = static_cast<int>(std::min<int64_t>(cdiv<int64_t>(a.max_tokens, 256), int64_t(sm_count) * 8));
-    return launch_ready<kv_slots_kernel>(dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, pdl, a);
+    const int64_t grid = std::min<int64_t>(cdiv<int64_t>(a.max_tokens, 256 * kSlotRun), int64_t(sm_count) * 4);
+    return launch_cluster<kv_slots_kernel>(dim3(static_cast<unsigned>(grid)), dim3(256), 1, size_t(a.batch + 1) * 4,
+                                           size_t(kKvPlanMaxBatch + 1) * 4, stream, pdl, a);
 }
 
 cudaError_t kv_plan_take_error(unsigned int* out) { return take_unit_error(out); }
