@@ -82,7 +82,12 @@ class Decoder:
         step = mnb.kv_step(after, self.table, new_start=start, tokens=total, max_new=max(counts))
         workspace = torch.empty(mnb.kv_attention_workspace_size(self.heads, self.kv_heads, self.dim, max(counts)),
                                 dtype=torch.uint8, device="cuda")
-        x = self.embedding[torch.tensor([t for seq in tokens for t in seq]).cuda()]
+        return self.run_layers([t for seq in tokens for t in seq], step, workspace)
+
+    def run_layers(self, ids, step, workspace):
+        """The logits (fp32) of a step's tokens."""
+        total = len(ids)
+        x = self.embedding[torch.tensor(ids).cuda()]
         q_end, k_end = self.heads * self.dim, (self.heads + self.kv_heads) * self.dim
         for layer in self.layers:
             qkv = layer["qkv"](self._norm(x))

@@ -1,8 +1,9 @@
 /*
  * mnb.h -- C ABI of the GB300 (sm_103a) library for block-quantized
  * weight-only matmul (MatMulNBits), the QMoE expert FFN built on it, and what
- * a decoder needs around them to generate: a paged key-value cache, attention
- * over it, and the verification of drafted tokens.
+ * a decoder needs around them to generate: a paged key-value cache (16-bit, or
+ * 8-bit codes with scales), the plan of a step's pages, attention over the
+ * cache, the logits' way to probabilities, and the verification of drafted tokens.
  *
  * Shared conventions
  * ------------------
@@ -517,6 +518,14 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * reads as zeros and records MNB_ERR_CONTENT.  So does a length past max_pages *
  * page_size: the new tokens keep their positions, and see those of their tokens
  * that have a page.
+ * Over 8-bit codes (any of the three dtypes) a value is code * scale, and the
+ * above holds with these changes: fp32 queries carry 22 bits as over an fp16
+ * cache; the probabilities carry 16 (fp32 output: 22) bits above 2^-33 (2^-27) of
+ * the row's largest, smaller ones err by 2^-50 of it, and where up to 64
+ * neighbouring tokens' value scales differ, the smaller ones' probabilities have
+ * these limits raised by the ratio to the largest.  A NaN code that a row sees gives
+ * NaN.  Scales of blocks without a visible token are not read; the others are
+ * finite and not negative (a scale that is not spoils the rows that see its block).
  * Made for a few new tokens per sequence (decoding, drafts): one pass over the
  * cache serves 64 rows, so that a prompt is right but re-reads it.  workspace
  * 256-byte aligned. */
