@@ -432,7 +432,7 @@ typedef struct {
  * before anything is taken, the first sequence's first page on top; the first
  * sequence takes first, from the top, so that a step that adds tokens and one
  * that drops the same tokens undo each other.  A sequence's new tokens are refused (none
- * are added; its kept tokens and its pages stay) where it needs more than
+ * are added, no page is taken; its kept tokens and their pages stay) where it needs more than
  * max_pages pages or 2^31 - 4097 tokens; else where it takes pages and the pages
  * asked for up to and with it are more than there are; or where the tokens asked
  * for up to and with it are more than max_tokens.  (What these sums count does

@@ -780,7 +780,7 @@ def token_probs(logits, rules, out, *, row_start=None, draft_tokens=None, mask=N
     st = load_library().token_probs(lp, _dtype_code(logits), ls, lr,
                                     _packed(row_start, "row_start", torch.int32, device, (batch + 1,)), tokens,
                                     _address(rules),
-                                    _packed(draft_tokens, "draft_tokens", torch.int32, device, (batch, rows - 1)), mp, ms,
+                                    _packed(draft_tokens, "draft_tokens", torch.int32, device, (batch, max(rows - 1, 0))), mp, ms,
                                     mr, rows, vocab, op, os_, orow, int(bool(softmax)), _stream_on(device, stream))
     if check:
         _check(st, "token_probs")

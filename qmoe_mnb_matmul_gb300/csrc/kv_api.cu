@@ -262,11 +262,11 @@ mnb_status token_probs(const void* logits, mnb_dtype dtype, int64_t logits_seq_s
                        const int32_t* draft_tokens, const uint32_t* mask, int64_t mask_seq_stride,
                        int64_t mask_row_stride, int64_t rows, int64_t vocab, float* out, int64_t out_seq_stride,
                        int64_t out_row_stride, int softmax, mnb_stream_t stream) {
-    if (!rules || !valid_dtype(dtype) || rules->batch < 0 || rows < 1 || vocab < 1 || rules->history_columns < 0 ||
+    if (!rules || !valid_dtype(dtype) || rules->batch < 0 || rows < 0 || vocab < 1 || rules->history_columns < 0 ||
         rules->biases < 0 || tokens < 0)
         return MNB_ERR_INVALID_ARG;
     const int64_t batch = rules->batch;
-    if (batch == 0) return MNB_OK;
+    if (batch == 0 || rows == 0) return MNB_OK;
     if ((!logits && !(row_start && tokens == 0)) || !out) return MNB_ERR_INVALID_ARG;
     if (rules->history && (!rules->history_lens || rules->history_stride < rules->history_columns)) return MNB_ERR_INVALID_ARG;
     if (rules->biases > 0 && (!rules->bias_tokens || !rules->bias_values || rules->bias_stride < rules->biases))

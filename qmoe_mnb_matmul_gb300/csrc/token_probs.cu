@@ -57,6 +57,20 @@ template <typename T>
 struct Raw {
     using V = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
     V v;
+    // -infinity for the values whose bit (of the low four) of `take` is 0: the product puts bit j on
+    // top of byte j, and a byte permutation spreads a byte's top bit
+    __device__ __forceinline__ void keep(uint32_t take) {
+        constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+        const uint32_t tops = (take & 0xFu) * 0x10204080u;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(V) / 4); ++j) {
+            uint32_t m;
+            const uint32_t spread = sizeof(T) == 4 ? 0x8888u + 0x1111u * j : j == 0 ? 0x9988u : 0xBBAAu;
+            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(m) : "r"(tops), "r"(spread));
+            w[j] = (w[j] & m) | (kNothing & ~m);
+        }
+    }
     __device__ __forceinline__ void widen(float (&x)[4]) const {
         alignas(16) T e[4];
         *reinterpret_cast<V*>(e) = v;
@@ -284,8 +298,18 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
         }
     }
 
-    // ---- the other tokens: x[j] = -inf where the value is not the passes' own (forbidden or
-    // listed).  The first `full` groups of a warp lie within the vocabulary, `last` is its part of the
+    if (FILTER) {
+        // the bits of the tokens that are the passes' own: allowed, and not listed
+        for (int w = tid; w < bit_words; w += kProbThreads) {
+            const int at = ((w >> 2) << ctas_log | static_cast<int>(rank)) * 4 + (w & 3);  // of the row's words
+            uint32_t own = mask == nullptr ? ~0u : at * 32 < vocab ? __ldg(mask + at) : 0u;
+            if (items > 0) own &= ~listed[w];
+            listed[w] = own;
+        }
+        __syncthreads();
+    }
+
+    // ---- the other tokens: x[j] = -inf where the value is not the passes' own.  The first `full` groups of a warp lie within the vocabulary, `last` is its part of the
     // chunk that the vocabulary ends in.
     const int whole = vocab >> 7, step = kProbWarps << ctas_log;
     const int full = whole > chunk(0) ? (whole - chunk(0) - 1) / step + 1 : 0;
@@ -296,21 +320,11 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
     const int64_t stride = static_cast<int64_t>(step) * 128;
     // bits of the four values that are the passes' own
     auto own_values = [&](int k) {
-        uint32_t take = 0xFu;
-        const int word = chunk(k) * 4, bit_word = (k * kProbWarps + warp) * 4;
-        if (VEC) {
-            if (mask) take = __ldg(mask + word + (lane >> 3)) >> (lane * 4 & 31) & 0xFu;
-            if (items > 0) take &= ~(listed[bit_word + (lane >> 3)] >> (lane * 4 & 31));
-        } else {
-            take = 0;
+        const uint32_t* words = listed + (k * kProbWarps + warp) * 4;
+        if (VEC) return words[lane >> 3] >> (lane * 4 & 31);
+        uint32_t take = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t bit = 1u;
-                if (mask && (chunk(k) * 128 + j * 32 < vocab)) bit = __ldg(mask + word + j) >> lane;
-                if (items > 0) bit &= ~(listed[bit_word + j] >> lane);
-                take |= (bit & 1u) << j;
-            }
-        }
+        for (int j = 0; j < 4; ++j) take |= (words[j] >> lane & 1u) << j;
         return take;
     };
     // all groups of this warp: each(x of the groups), N groups loaded at a time; `write`: what
@@ -334,13 +348,8 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
             }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
+                if (FILTER) raw[m].keep(own_values(k0 + m));
                 raw[m].widen(x[m]);
-                // (what is stored over later need not be left out, but a pass that skips it
-                // where it can took 86 us instead of 70)
-                if (!FILTER) continue;
-                const uint32_t take = own_values(k0 + m);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[m][j] = take >> j & 1u ? x[m][j] : -INFINITY;
             }
             each(k0, x);
             if (write)
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
         for (; k < full; ++k) some(k, Count<1>{});
         if (last) {
             float x[1][4];
-            const uint32_t take = FILTER && (!VEC || place(full, 0) < vocab) ? own_values(full) : 0xFu;
+            const uint32_t take = FILTER ? own_values(full) : 0xFu;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 x[0][j] = place(full, j) < vocab && (take >> j & 1u) ? to_f32(logits[place(full, j)]) : -INFINITY;
@@ -452,15 +461,14 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
     if (ctas > 1) cluster_wait();
 }
 
-// Listed tokens that a CTA may have, and the bytes of its bits and lists.
+// Listed tokens that a CTA may have, and the bytes of its bits and lists (of the bits alone, for a mask).
 struct ProbPlan {
     int64_t items, bytes;
 };
 ProbPlan plan_probs(int64_t vocab, int64_t listed, int cluster) {
     const int64_t tokens = cdiv<int64_t>(vocab, int64_t(cluster) * kProbWarps * 128) * kProbWarps * 128;
-    if (listed == 0) return {0, 0};
     const int64_t items = std::min(listed, tokens);
-    return {items, tokens / 32 * 8 + items * 8};
+    return {items, tokens / 32 * (listed > 0 ? 8 : 4) + items * 8};
 }
 
 template <typename T, bool VEC>
@@ -502,7 +510,7 @@ cudaError_t launch_token_probs(const ProbArgs& a, int dtype, int sm_count, bool 
     while (cluster < kProbCluster && plan_probs(a.vocab, listed, cluster).bytes > kProbMostSmem / 2) cluster <<= 1;
     const ProbPlan plan = plan_probs(a.vocab, listed, cluster);
     const dim3 grid(static_cast<unsigned>(a.batch * a.rows * cluster));
-    const size_t smem = static_cast<size_t>(plan.bytes);
+    const size_t smem = listed > 0 || a.mask ? static_cast<size_t>(plan.bytes) : 0;
     const int items = static_cast<int>(plan.items);
     if (dtype == kF32) return launch_type<float>(a, vec, grid, cluster, smem, items, pdl, stream);
     if (dtype == kF16) return launch_type<__half>(a, vec, grid, cluster, smem, items, pdl, stream);

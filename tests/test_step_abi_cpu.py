@@ -52,7 +52,7 @@ def probs(lib, logits=FAKE, dt=0, ls=5000, lr=1000, start=None, tokens=0, drafts
 
 def test_probs_errors(real):
     assert real.token_probs(FAKE, 0, 1, 1, None, 0, None, None, None, 0, 0, 1, 1, FAKE, 1, 1, 1, None) == INVALID
-    for bad in (dict(logits=None), dict(out=None), dict(dt=3), dict(dt=-1), dict(batch=-1), dict(rows=0), dict(vocab=0),
+    for bad in (dict(logits=None), dict(out=None), dict(dt=3), dict(dt=-1), dict(batch=-1), dict(rows=-1), dict(vocab=0),
                 dict(ls=-1), dict(lr=-1), dict(ms=-1), dict(mr=-1), dict(orow=999), dict(os=10), dict(tokens=-1),
                 dict(history=FAKE, history_columns=5, history_stride=5), dict(history_columns=-1), dict(biases=-1),
                 dict(history=FAKE, history_lens=FAKE, history_columns=5, history_stride=4),
@@ -73,6 +73,7 @@ def test_probs_errors(real):
                 dict(start=FAKE, tokens=1 << 40, lr=1 << 40)):
         assert probs(real, **bad) == OVERFLOW, bad
     assert probs(real, batch=0, logits=None, out=None) == OK
+    assert probs(real, rows=0, logits=None, out=None) == OK
 
 
 # ------------------------------------------------------------------ the binding

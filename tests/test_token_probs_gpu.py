@@ -111,7 +111,7 @@ def check(out, r, softmax=True, rel=REL, rows=None):
 @pytest.mark.parametrize("B,R,V,history,biases,mask", [
     (1, 1, 1, 0, 0, False), (2, 1, 3, 5, 2, True), (1, 5, 151936, 2000, 0, False), (3, 2, 50257, 100, 300, True),
     (5, 3, 997, 50, 16, True), (2, 2, 2048, 0, 7, False), (2, 2, 2049, 9, 0, True), (1, 2, 163841, 30, 3, False),
-    (1, 1, 400000, 3000, 1, True), (2, 4, 32768, 1, 0, False), (1, 1, 163968, 0, 0, True)])
+    (1, 1, 400000, 3000, 1, True), (1, 1, 400000, 30000, 2047, False), (3, 1, 262144, 20000, 9, True), (2, 4, 32768, 1, 0, False), (1, 1, 163968, 0, 0, True)])
 def test_probabilities(dtype, B, R, V, history, biases, mask):
     r = inputs(B * 1000 + R, B, R, V, dtype, history, biases, mask)
     out = torch.full((B, R, V), 7.0, device="cuda")
@@ -239,10 +239,33 @@ def test_no_rules_no_history_and_no_rows():
     mnb.token_probs(logits, mnb.token_rules(history=empty, history_lens=lens, bias_tokens=empty,
                                             bias_values=empty.float()), out)
     check(out, {"logits": logits})
+    none = torch.empty((2, 0, 777), device="cuda")
+    mnb.token_probs(none, mnb.token_rules(batch=2), none)
     out.fill_(3.0)
     mnb.token_probs(torch.empty((0, 777), device="cuda"), mnb.token_rules(batch=2), out,
                     row_start=torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert (out == 3.0).all()
+
+
+def test_heavily_repeated_and_neighbouring_tokens():
+    """Histories of one token and of a run of neighbours, the same token in the biases again and again, all of it in one
+    CTA's words; counts stay whole numbers."""
+    V, n = 151936, 6000
+    g = torch.Generator("cuda").manual_seed(3)
+    history = torch.stack([torch.full((n,), 7, device="cuda"), torch.arange(n, device="cuda") % 128,
+                           torch.arange(n, device="cuda"), torch.full((n,), V - 1, device="cuda")]).to(torch.int32)
+    r = {"logits": torch.randn((4, 2, V), generator=g, device="cuda"), "history": history,
+         "history_lens": torch.full((4,), n, dtype=torch.int32, device="cuda"),
+         "frequency": torch.full((4,), 2.0 ** -8, device="cuda"), "presence": torch.full((4,), 0.25, device="cuda"),
+         "repetition": torch.full((4,), 1.25, device="cuda"),
+         "bias_tokens": torch.full((4, 900), 7, dtype=torch.int32, device="cuda"),
+         "bias_values": torch.linspace(-3, 3, 900, device="cuda").repeat(4, 1).contiguous(),
+         "draft_tokens": torch.full((4, 1), 7, dtype=torch.int32, device="cuda")}
+    out = torch.empty((4, 2, V), device="cuda")
+    mnb.token_probs(r["logits"], rules(r, 4), out, draft_tokens=r["draft_tokens"])
+    check(out, r)
+    mnb.token_probs(r["logits"], rules(r, 4), out, draft_tokens=r["draft_tokens"], softmax=False)
+    check(out, r, softmax=False, rel=6 * 64 * 2.0 ** -24)
 
 
 def test_captured_beside_an_eager_call_and_on_another_stream():
