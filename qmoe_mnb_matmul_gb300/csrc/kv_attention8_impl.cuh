@@ -14,13 +14,15 @@
 // to eight rows take tiles of 128 tokens, as many bytes as 64 of 16 bits, others tiles of
 // 64 (their registers hold the scores of no more).
 //
-// Codes to operands.  e4m3 converts exactly to fp16, two codes an instruction.  ldmatrix
-// moves 16-bit elements, that is pairs of codes: a lane gets four neighbouring codes of
-// a key, where the instruction wants two pairs eight apart; the order of the head
-// dimension is free as long as the queries' matches, so they are loaded as the codes lie
-// (step of 16, lane qc: elements 4 qc .. 4 qc + 3).  Transposed, a lane gets two tokens'
-// pairs (d, d + 1); one byte permutation makes a pair of tokens for d and one for d + 1,
-// and rows quad and quad + 8 of the product are then columns 2 quad and 2 quad + 1.
+// Codes to operands.  e4m3 converts exactly to fp16, two codes an instruction.  A key tile
+// comes by ldmatrix of 16-bit elements, that is pairs of codes: a lane gets four
+// neighbouring codes of a key, where the instruction wants two pairs eight apart; the order
+// of the head dimension is free as long as the queries' matches, so they are loaded as the
+// codes lie (step of 16, lane qc: elements 4 qc .. 4 qc + 3).  A value tile comes by
+// ldmatrix's transposed 16 x 16 matrices of bytes: a lane gets four neighbouring tokens of
+// a column.  The order of a block's sixteen tokens is free likewise, as long as the
+// weights' matches: row m of the score product is token_of(m), so that the lane's four
+// tokens are its four places along the value product.
 //
 // Rounding.  Queries of every type are scaled by a power of two per row to a largest
 // magnitude in [2^14, 2^15) and go in as fp16: one part for 16-bit queries (exact for
@@ -88,6 +90,18 @@ __device__ __forceinline__ uint32_t halves_high(uint32_t codes) {
     uint32_t h;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(h) : "r"(codes));
     return h;
+}
+
+// The token (of sixteen) in row m of a score product.
+__device__ __forceinline__ int token_of(int m) { return (m & 6) * 2 + (m & 1) + (m >> 3) * 2; }
+
+// Two transposed 16 x 16 matrices of bytes: from a 16-byte row per lane (0 .. 15 the first one's), lane
+// l gets rows 4 (l % 4) .. + 3 of columns l / 4 (r[0]), l / 4 + 8 (r[1]), and the second one's.
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Bytes of the codes among four that are NaN (0x7F, 0xFF).
@@ -363,7 +377,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
             for (int x = 0; x < 2; ++x) c[g][x] = factor(sm.row_unit[row0 + g * 8 + qc * 2 + x]);
     }
 
-    float o[ND][RG][4];  // columns 2 quad, 2 quad + 1 of each sixteen; rows 2 qc, 2 qc + 1 of each eight
+    float o[ND][RG][4];  // columns quad, quad + 8 of each sixteen; rows 2 qc, 2 qc + 1 of each eight
     float m[RG][2], l[RG][2];  // weights so far are 2^(score - m), l their sum
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
@@ -376,9 +390,10 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
     }
     const bool active = row0 < w.t.rows;  // a warp whose rows are all padding only keeps the barriers
     int tok0 = (w.t.lo / TILE + w.tile) * TILE + wt * TOK;  // the warp's first token
-    // This lane's ldmatrix row in a key or value tile: 16 tokens of two 16-byte chunks.
+    // This lane's ldmatrix row in a key and a value tile: 16 tokens of two 16-byte chunks.
     // Chunk c + 2 i of the row is the address of chunk c XOR 32 i within a panel.
-    const uint32_t t_lane = tile_at(TILE, wt * TOK + (lane & 15), lane >> 4);
+    const uint32_t k_lane = tile_at(TILE, wt * TOK + token_of(lane & 15), lane >> 4);
+    const uint32_t v_lane = tile_at(TILE, wt * TOK + (lane & 15), lane >> 4);
     const uint8_t* q_lane = sm.q + (row0 + quad) * P::kQRow + qc * 8;
 #pragma unroll 1
     for (int i = 0; i < nt; ++i, tok0 += TILE) {
@@ -402,17 +417,15 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                     if constexpr (QF32 || kTwo) s2[t][g][x] = 0.f;
                 }
         if (ok) ok = tile_wait(&sm.k_full[kring.slot], kring.parity);
-        float ka[MT][2], vb[MT][2];  // scales of keys and values, tokens quad and quad + 8 of each block
+        float ka[MT], vb[MT];  // scales of keys and values: the lane's tokens of a block lie in one half of it
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const float* at = sm.scales + kring.slot * 32 + wt * (TOK / 8) + 2 * t + y;
-                ka[t][y] = at[0];
-                vb[t][y] = at[16];
-            }
+        for (int t = 0; t < MT; ++t) {
+            const float* at = sm.scales + kring.slot * 32 + wt * (TOK / 8) + 2 * t + (quad >> 2);
+            ka[t] = at[0];
+            vb[t] = at[16];
+        }
         if (active && !none) {
-            const uint32_t kt = smem_u32(sm.k + kring.slot * P::kSlotBytes) + t_lane;
+            const uint32_t kt = smem_u32(sm.k + kring.slot * P::kSlotBytes) + k_lane;
 #pragma unroll
             for (int kp = 0; kp < KS / 2; ++kp) {  // two steps along the head dimension
                 uint32_t qb[2][PQ][RG][2];
@@ -464,7 +477,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         if constexpr (QF32 || kTwo) s[t][g][x] += s2[t][g][x];
-                        s[t][g][x] *= ka[t][x >> 1];
+                        s[t][g][x] *= ka[t];
                     }
         }
         tile_free(&sm.k_empty[kring.slot], lane);
@@ -475,7 +488,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
             vring.next();
             continue;
         }
-        // ---- mask, running maximum and sum.  s[t][g][x]: token 16 t + quad + 8 (x / 2), row 2 qc + x % 2
+        // ---- mask, running maximum and sum.  s[t][g][x]: token 16 t + token_of(quad + 8 (x / 2)), row 2 qc + x % 2
         if (edge) {
 #pragma unroll
             for (int g = 0; g < RG; ++g)
@@ -487,7 +500,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const int j = tok0 + t * 16 + quad + 8 * y;
+                            const int j = tok0 + t * 16 + token_of(quad + 8 * y);
                             if (j < lo || j >= hi) s[t][g][2 * y + x] = -INFINITY;
                         }
                 }
@@ -495,13 +508,12 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
         // a power of two above the warp's largest value scale, and the scales over it
         float b = 0.f;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) b = fmaxf(b, fmaxf(vb[t][0], vb[t][1]));
+        for (int t = 0; t < MT; ++t) b = fmaxf(b, vb[t]);
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
         const uint32_t be = min(__float_as_uint(b) >> 23, 252u);
         b = __uint_as_float((be + 1u) << 23);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) vb[t][y] *= __uint_as_float((253u - be) << 23);
+        for (int t = 0; t < MT; ++t) vb[t] *= __uint_as_float((253u - be) << 23);
         float f[RG][2];
         uint32_t pb[MT][RG][PP][2];  // P^T in fp16 parts, as the B operand
 #pragma unroll
@@ -531,7 +543,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                         float& e = s[t][g][2 * y + x];
                         e = exp2_approx(fmaf(e, c[g][x], -ref[x]));
                         sum[x] += e;
-                        e *= vb[t][y];
+                        e *= vb[t];
                     }
                     uint32_t parts[PP];
                     split<kF16, PP, kF16Up>(s[t][g][2 * y], s[t][g][2 * y + 1], parts);
@@ -581,9 +593,8 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll 1
                         for (int e = 0; e < TOK; ++e) {
                             const int j = tok0 + e;
-                            const uint32_t v =
-                                *reinterpret_cast<const uint16_t*>(vtile + tile_at(TILE, wt * TOK + e, n) + quad * 2);
-                            const uint32_t bad = nan_codes(v);
+                            const uint8_t* v = vtile + tile_at(TILE, wt * TOK + e, n) + quad;
+                            const uint32_t bad = nan_codes(v[0] | v[8] << 8);
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 if (!(bad >> (8 * y) & 1u)) continue;
@@ -604,22 +615,18 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
         }
         // ---- O^T = f O^T + b V^T P^T
         if (active) {
-            const uint32_t vt = smem_u32(vtile) + t_lane;
+            const uint32_t vt = smem_u32(vtile) + v_lane;
 #pragma unroll
             for (int np = 0; np < ND / 2; ++np) {  // 32 columns
                 uint32_t r[MT][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    ldsm_t((vt ^ ((np & 3) << 5)) + (np >> 2) * (TILE * 128) + t * 2048, r[t]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r[t][k] = __byte_perm(r[t][k], 0u, 0x3120);
-                }
+                for (int t = 0; t < MT; ++t) ldsm_bytes_t((vt ^ ((np & 3) << 5)) + (np >> 2) * (TILE * 128) + t * 2048, r[t]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     float z[PP][RG][4] = {};
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        const uint32_t v16[4] = {halves(r[t][2 * y]), halves_high(r[t][2 * y]), halves(r[t][2 * y + 1]),
+                        const uint32_t v16[4] = {halves(r[t][2 * y]), halves(r[t][2 * y + 1]), halves_high(r[t][2 * y]),
                                                  halves_high(r[t][2 * y + 1])};
 #pragma unroll
                         for (int p = PP - 1; p >= 0; --p)
@@ -694,11 +701,8 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
             for (int n = 0; n < ND / 2; ++n)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float (&from)[4] = o[half * (ND / 2) + n][g];
-                    *reinterpret_cast<float2*>(mine + (qc * 2 + x) * P::kMergeRow + n * 16 + 2 * quad) =
-                        make_float2(from[x], from[2 + x]);
-                }
+                for (int x = 0; x < 4; ++x)
+                    mine[(qc * 2 + (x & 1)) * P::kMergeRow + n * 16 + quad + 8 * (x >> 1)] = o[half * (ND / 2) + n][g][x];
             compute_sync();
 #pragma unroll 1
             for (int i = threadIdx.x; i < 8 * WR * V4; i += 32 * kComputeWarps) {

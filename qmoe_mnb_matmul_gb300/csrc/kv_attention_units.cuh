@@ -154,6 +154,12 @@ struct Costs16 {
     static __device__ __forceinline__ int of(int rows) { return ROWS > 32 && rows > 32 ? 2 : 1; }
 };
 
+// Tiles that `units` reach into, at `cost` units each.
+template <typename COSTS, typename N>
+__device__ __forceinline__ N tiles_in(N units, int cost) {
+    return COSTS::kMost == 2 ? (units + cost - 1) >> (cost - 1) : (units + cost - 1) / cost;
+}
+
 // A row tile of one sequence: what its rows may see.
 struct RowTile {
     int first_row;  // flat index (token * group + head) of the tile's first row
@@ -350,7 +356,7 @@ __device__ __forceinline__ Range find_range(const KvAttnArgs& a, Walk& w) {
     if (COSTS::kMost > 1) {
         // (w.tile counts units) a tile belongs to the CTA that its first unit falls to
         const int unit = w.tile, cost = w.t.cost;
-        w.tile = (unit + cost - 1) / cost;
+        w.tile = tiles_in<COSTS>(unit, cost);
         r.at += w.tile * cost - unit;
         if (w.tile == w.t.tiles && r.at < r.end) {
             next_pair<ROWS, TILE, COSTS>(a, w);
@@ -366,7 +372,7 @@ __device__ __forceinline__ int part_tiles(const Walk& w, int64_t units) {
     if (COSTS::kMost > 1) {
         // (units past the pair's end do not matter: a division in 32 bits)
         const int some = static_cast<int>(min(units, static_cast<int64_t>(0x7fffffff - COSTS::kMost)));
-        units = (some + w.t.cost - 1) / w.t.cost;
+        units = tiles_in<COSTS>(some, w.t.cost);
     }
     return static_cast<int>(min(static_cast<int64_t>(w.t.tiles - w.tile), units));
 }
