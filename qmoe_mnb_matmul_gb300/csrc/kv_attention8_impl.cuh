@@ -110,10 +110,13 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
     return (top >> 7) * 0xFFu;
 }
 
-__device__ __forceinline__ float load_now(const float* p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
+// Asynchronous copy of a float to shared memory (`take` false: a zero, nothing is read), and the
+// arrival at a barrier once this thread's copies have landed (one of the barrier's count).
+__device__ __forceinline__ void copy_float(float* dst, const float* src, bool take) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_with_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Page and row of a token that moves on by a tile at a time.
@@ -140,9 +143,11 @@ struct Cursor {
 
 // The key or the value tiles of the CTA's range, by one warp: lane l issues the box of
 // row block l % blocks and panel l / blocks of every tile (32 boxes at most) and looks up
-// its page itself, one tile ahead.  SCALES: lane l also brings the key scale (the upper
-// sixteen lanes the value scale) of tokens 8 (l % 16) .. + 7 of the tile, looked up one
-// tile ahead, its page two tiles: both arrive with the key tile.
+// its page itself, one tile ahead.  SCALES: lane l also copies the key scale (the upper
+// sixteen lanes the value scale) of tokens 8 (l % 16) .. + 7 of the tile into the slot, its page
+// looked up one tile ahead; both arrive with the key tile.  (Through a register, asked for
+// one tile ahead, the scales' way from HBM was a tile's time: tile times a few percent longer; heads of 64, 64
+// sequences of 1 .. 8192 tokens.)
 template <int DP, int ROWS, bool QF32, int SLOTS, bool SCALES>
 __device__ __forceinline__ void produce8(const KvAttnArgs& a, const CUtensorMap* map, uint8_t* slots, float* scales,
                                          uint64_t* full, uint64_t* empty, Walk w, const Range& r) {
@@ -166,50 +171,39 @@ __device__ __forceinline__ void produce8(const KvAttnArgs& a, const CUtensorMap*
         const int nt = part_tiles<Costs8<ROWS>>(w, r.end - at);
         bad = bad || w.pos0 + w.count > a.step.capacity;
         const int first = (w.t.lo / TILE + w.tile) * TILE;
-        Cursor box, mine;  // of the boxes, and of the scales (two tiles ahead)
+        Cursor box, mine;  // of the boxes, and of the scales
         box.start(a, w, first + row0);
         mine.start(a, w, first + unit * 8);
         // boxes that no row sees are asked for outside the cache, which fills them with
         // zeros and reads nothing; scales likewise
         auto wanted = [&] { return issues && box.tok < w.t.hi && box.tok + R > w.t.lo; };
         auto seen = [&](int tok) { return scaled && tok < w.t.hi && tok + 8 > w.t.lo; };
-        auto scale_of = [&](int page, int row) {
-            if (page < 0 || page >= a.cache.num_pages) return 0.f;
-            return load_now(table + page * a.cache.scale_page_stride + w.h * a.cache.scale_head_stride +
-                            (row >> a.cache.block_shift));
-        };
         int page = wanted() ? load_now(box.page) : -1;
-        float scale = 0.f;
-        int row1 = 0, page1 = -1;  // of the scale of the tile ahead
-        if (SCALES) {
-            const int page0 = seen(mine.tok) ? load_now(mine.page) : -1, row_0 = mine.row;
-            mine.template next<TILE>(a, step_pages, step_rows);
-            row1 = mine.row;
-            page1 = nt > 1 && seen(mine.tok) ? load_now(mine.page) : -1;
-            scale = scale_of(page0, row_0);
-        }
+        int scale_page = SCALES && seen(mine.tok) ? load_now(mine.page) : -1;
         for (int i = 0; i < nt; ++i) {
             const int cur = page, cur_row = box.row;
             const bool outside = wanted() && (cur < 0 || cur >= a.cache.num_pages);
             box.template next<TILE>(a, step_pages, step_rows);
             page = i + 1 < nt && wanted() ? load_now(box.page) : -1;
-            float ahead = 0.f;
+            const float* scale = table;
+            bool scale_there = false;
             if (SCALES) {
-                ahead = scale_of(page1, row1);
+                scale_there = scale_page >= 0 && scale_page < a.cache.num_pages;
+                if (scale_there)
+                    scale += scale_page * a.cache.scale_page_stride + w.h * a.cache.scale_head_stride +
+                             (mine.row >> a.cache.block_shift);
                 mine.template next<TILE>(a, step_pages, step_rows);
-                row1 = mine.row;
-                page1 = i + 2 < nt && seen(mine.tok) ? load_now(mine.page) : -1;
+                scale_page = i + 1 < nt && seen(mine.tok) ? load_now(mine.page) : -1;
             }
             if (ok) ok = warp_wait(&empty[ring.slot], ring.parity ^ 1);  // the first round passes at once
             if (!ok) break;
             __syncwarp();  // the slot's scales were read, too
             if (issues) tma_load_4d(dst + ring.slot * P::kSlotBytes, map, panel * 128, cur_row, w.h, cur, &full[ring.slot]);
             if (SCALES) {
-                scales[ring.slot * 32 + lane] = scale;
-                scale = ahead;
+                copy_float(scales + ring.slot * 32 + lane, scale, scale_there);
+                arrive_with_copies(&full[ring.slot]);
             }
-            __syncwarp();
-            // (the copies may land before the barrier expects them: its one arrival is this)
+            // (the tile may land before the barrier expects it: this arrival is still to come)
             if (lane == 0) mbar_arrive_expect_tx(&full[ring.slot], P::kSlotBytes);
             bad = bad || outside;
             ++issued;
@@ -772,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < KSLOTS; ++s) {
-            mbar_init(&k_full[s], 1);
+            mbar_init(&k_full[s], 1 + 32);  // the tile's, and a scale's per lane
             mbar_init(&k_empty[s], kComputeWarps);
         }
         for (int s = 0; s < VSLOTS; ++s) {
