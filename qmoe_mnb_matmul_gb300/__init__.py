@@ -1,6 +1,7 @@
 """GB300-native block-quantized weight-only matmul (MatMulNBits INT4/INT3) and
-the QMoE expert FFN built on it, with the paged key-value cache, the attention
-over it and the draft verification that a decoder needs around them.
+the QMoE expert FFN built on it, with the paged key-value cache (16-bit or 8-bit
+codes), the plan of its pages, the attention over it, the token probabilities and
+the draft verification that a decoder needs around them.
 
 The compute lives in the CUDA library ``_build/libmnb.so`` (hand-written
 sm_103a kernels behind the C ABI of ``include/mnb.h``); this package is its

@@ -11,7 +11,7 @@
 // rounded likewise.  Scales are powers of two because e4m3 keeps its precision over them:
 // a finer scale gains nothing above the subnormal codes, and a grown scale that is a
 // multiple of the old one by a power of two moves older codes without rounding them
-// again, down to the subnormal ones (448 / 2^15: 2^-14.8 of the block's largest).
+// again, down to the subnormal ones (below 2^-6: 2^-14.8 of a block's largest code).
 //
 // Work.  A unit is a block that the step touches: sequence b's k-th one has the number
 // new_start[b] / rows + 2 b + k, which no two share (n tokens touch at most n / rows + 2
@@ -20,9 +20,15 @@
 // values, a lane eight elements of a row as two runs of four that a rotation pairs, and
 // holds the warp's tokens in 64 registers between the largest value and the rounding.
 // Queries have CTAs of their own behind the units' (a launch of their own, with twice the
-// warps on an SM, made prompts of 16920 tokens 92 us instead of 83).
+// warps on an SM, made prompts of 16920 tokens 92 us instead of 83).  The rows' angles are
+// neighbours in the table: one bulk copy per block brings them to shared memory.
 //
-// Bound: HBM for prompts, three dependent loads for one token.
+// Bound: instruction issue (57 %, 24 instructions an element over all) and load latency for
+// prompts, three dependent loads for one token.
+//
+// Measured: one token of 16 + 8 + 8 heads of 128 in fp32 4.9 us, 190 drafts of 64 sequences 7.5
+// us; prompts of 16920 tokens in bf16 74 us, 3.4 TB/s (251 MB).  Sixteen tokens a warp at
+// 128 registers took 110 us, angles from global memory 3 us more of a short call.
 #include <algorithm>
 
 #include "common.cuh"
