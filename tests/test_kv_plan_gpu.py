@@ -110,7 +110,7 @@ class Pool:
 @pytest.mark.parametrize("batch,page,columns,most,spare,inplace", [
     (1, 16, 4, 1, 0, False), (1, 16, 400, 5000, 400, True), (7, 8, 9, 20, 3, False), (64, 16, 30, 5, 40, True),
     (64, 24, 30, 100, 90, False), (257, 128, 12, 700, 300, True), (1000, 16, 60, 400, 5000, False),
-    (1031, 32, 8, 3, 100, True), (1, 1, 50, 40, 60, False), (5000, 8, 4, 12, 2000, False)])
+    (1031, 32, 8, 3, 100, True), (1, 1, 50, 40, 60, False), (5000, 8, 4, 12, 2000, False), (8192, 8, 3, 9, 3000, True)])
 def test_steps_in_a_row(batch, page, columns, most, spare, inplace):
     r = random.Random(batch * 31 + page)
     pool = Pool([r.randint(0, columns) for _ in range(batch)], columns, spare, page, seed=batch, stride=columns + batch % 3)
