@@ -36,8 +36,8 @@
 // ratio takes from the 2^-51.
 //
 // Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens, 16 query
-// heads over 8, 545 MB: 99 us, 5.5 TB/s (fp32 queries 96; heads of 64, half the bytes, 73; of
-// 256, 4 over 16, 54); one sequence of 131072 tokens, 32 over 4, 134 MB: 34 us; 777 tokens: 7.9 us, all
+// heads over 8, 545 MB: 95 us, 5.7 TB/s (fp32 queries 96; heads of 64, half the bytes, 74; of
+// 256, 4 over 16, 54); one sequence of 131072 tokens, 32 over 4, 134 MB: 33.5 us; 777 tokens: 7.9 us, all
 // latency.  A tile takes 1.3 us and 0.2 us more per 4 KB of it: bound by the chain of a
 // tile's steps in two compute warps per scheduler (issue slots 48 % busy), not by the
 // tensor pipe (22 %) or HBM.  16 sequences with 1 .. 5 drafts, 8 .. 40 rows, 147 MB: 88 us (spills
@@ -79,13 +79,14 @@ struct Plan8 {
 };
 
 // What a pair costs besides its tiles (its queries, the first tile's way, the join of the
-// warps, the store), in tiles: 64 sequences of 1 .. 8192 tokens 136 us with none, 117 with
-// one, 107 with two, 99 with three, 97 with four; 8 of 2000 tokens 15.0 with three, 15.5 with four.
+// warps, the store), in tiles.  64 sequences of 1 .. 8192 tokens: 136 us with none, 117 with
+// one, 108 with two, 100 with three, 95 with four and more; 8 of 2000 tokens 14.8 with two
+// and three, 15.5 with four; 200 of 10 .. 300 48.8, 47.6, 48.5 with two, three, four.
 // With more rows a tile's cost grows with them (of 64 tokens: 4 units up to 8 rows, 12 for 33 and
 // more): 16 sequences of 4 .. 20 rows, heads of 80, 50 us with one unit for all, 42 with these.
 template <int ROWS>
 struct Costs8 {
-    static constexpr int kMost = ROWS == 8 ? 1 : ROWS == 32 ? 7 : 12, kPair = ROWS == 8 ? 3 : 16;
+    static constexpr int kMost = ROWS == 8 ? 1 : ROWS == 32 ? 7 : 12, kPair = ROWS == 8 ? 4 : 16;
     static __device__ __forceinline__ int of(int rows) {
         return ROWS == 8 ? 1 : rows <= 8 ? 4 : rows <= 16 ? 5 : rows <= 32 ? 7 : 12;
     }
