@@ -23,13 +23,13 @@
 // probability stored over what the second pass wrote.  Counts are whole numbers, of
 // several biases of a token the largest number stays, and the array's order is that of the bits: no
 // result depends on the order of the atomics.  (One word per token in the passes
-// themselves, changed where a thread meets it: 165 us instead of 70 for 64 sequences of up
+// themselves, changed where a thread meets it: 165 us instead of 73 for 64 sequences of up
 // to 6 rows.)  A warp takes 128 neighbouring tokens at a time and the next 128 belong
 // to another CTA: a vocabulary's frequent tokens are neighbours.
 //
 // Measured (151936 entries): one sequence of 5 fp32 rows with 2000 tokens of history 9.8 us (one
 // row without lists 6.1), 64 sequences of up to 6 bf16 rows with 3000 tokens, biases and
-// masks, 208 MB: 72 us, 2.9 TB/s; 64 fp32 rows without lists, 78 MB: 23 us.  A row has three phases with
+// masks, 208 MB: 73 us, 2.8 TB/s; 64 fp32 rows without lists, 78 MB: 23 us.  A row has three phases with
 // a barrier of its cluster between them, and two CTAs of 512 threads per SM do not
 // cover each other's (issue 46 %, DRAM 32 %, 89 MB read for 67).  256 threads, 1024, and three or four
 // CTAs per SM with fewer registers were slower, one kernel that keeps the row in registers too (245 us).
