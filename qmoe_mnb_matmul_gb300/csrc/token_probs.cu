@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
     const int64_t b = row / a.rows;
     const T* logits = static_cast<const T*>(a.logits);
     if (a.row_start) {
-        const int r0 = __ldg(a.row_start + b), r1 = __ldg(a.row_start + b + 1), r = r0 + i;
+        const int64_t r0 = __ldg(a.row_start + b), r1 = __ldg(a.row_start + b + 1), r = r0 + i;  // (r passes 32 bits where r0 ends there)
         if (r0 < 0 || r >= r1 || r >= a.tokens) return;  // (the whole cluster)
         logits += r * a.logits_row;
     } else {
