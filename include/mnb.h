@@ -523,7 +523,9 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * cache; the probabilities carry 16 (fp32 output: 22) bits above 2^-33 (2^-27) of
  * the row's largest, smaller ones err by 2^-50 of it, and where up to 64
  * neighbouring tokens' value scales differ, the smaller ones' probabilities have
- * these limits raised by the ratio to the largest.  A NaN code that a row sees gives
+ * these limits raised by the ratio to the largest (whether the row sees its token
+ * or not).  Values of any size give finite sums; a value past fp32's largest
+ * number counts as it is, up to the rounding of out.  A NaN code that a row sees gives
  * NaN.  Scales of blocks without a visible token are not read; the others are
  * finite and not negative (a scale that is not spoils the rows that see its block).
  * Made for a few new tokens per sequence (decoding, drafts): one pass over the

@@ -105,6 +105,13 @@ __device__ __forceinline__ float kv_log_sum(float reference, float sum, int shif
 }
 #endif
 
+// Over 8-bit codes: once a warp meets a value scale above 2^64, it holds its rows' sums of weights
+// times values 2^-64 times as large.  Weights of up to 2^15, codes below 2^9 and 2^31 tokens
+// then stay below 2^119 whatever the scales (held alike for all, a single value of 2^113 was
+// too large).  The workspace says so by a negative sum of weights.
+constexpr int kKvFarPower = 64;
+constexpr float kKvFarDown = 1.f / 18446744073709551616.f;
+
 struct KvAttnArgs {
     KvCache cache;
     KvStep step;

@@ -48,12 +48,12 @@ namespace {
 constexpr int kFewParts = 16;
 constexpr int kJoinGridY = 16;  // CTAs of a pair
 
-// Writes columns d, d + 1 of a row (lane's share of it) and the row's log-sum-exp.
+// Writes columns d, d + 1 of a row (lane's share of it, `far` 2^-64 times as large) and the row's log-sum-exp.
 __device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, int flat, int head_kv, int d, float2 s,
-                                           float m, float l) {
+                                           float m, float l, bool far) {
     const int tok = a.by_group(flat), head = head_kv * a.group + flat - tok * a.group;
     const int64_t token = tok;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+    const float inv = (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * (far ? 1.f / kKvFarDown : 1.f);  // NaN stays NaN
     if (d < a.cache.dim) {
         const int64_t at = token * a.out_stride + static_cast<int64_t>(head) * a.cache.dim + d;
         store_from_f32(a.out, out_dtype, at, s.x * inv);
@@ -64,11 +64,12 @@ __device__ __forceinline__ void join_store(const KvAttnArgs& a, int out_dtype, i
             kv_log_sum(m, l, kv_weight_shift(a.cache.dtype));
 }
 
-// A part's weight.  Never zero: a part with an infinite column adds that infinity
-// however small its weight (2^-126 of anything finite changes nothing).
-__device__ __forceinline__ float part_weight(float reference, float largest) {
+// A part's weight.  Over 16-bit values never zero: a part with an infinite column adds that infinity
+// however small its weight (2^-126 of anything finite changes nothing).  Codes have no
+// infinities, and of their sums, as large as 2^119, it would change something.
+__device__ __forceinline__ float part_weight(float reference, float largest, bool codes) {
     const float w = exp2f(reference - largest);
-    return w < 1.17549435e-38f ? 1.17549435e-38f : w;  // (NaN stays NaN)
+    return !codes && w < 1.17549435e-38f ? 1.17549435e-38f : w;  // (NaN stays NaN)
 }
 
 template <int DP>
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
     const int4 j = a.join[c];
     if (j.x < 0) return;
     const int n = j.x - c + 1, rows = j.y >> 1, slot0 = 2 * c + (j.y & 1), head_kv = j.w;
+    const bool codes = a.cache.dtype == MNB_E4M3;  // (a negative sum of weights: kKvFarDown)
     if (rows > kJoinGridY && n <= kFewParts) {
 #pragma unroll 1
         for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
@@ -95,8 +97,10 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
             float m = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float w = lane < n ? part_weight(ml.x, m == -INFINITY ? 0.f : m) : 0.f;
-            const float l = warp_sum(w * ml.y);
+            float w = lane < n ? part_weight(ml.x, m == -INFINITY ? 0.f : m, codes) : 0.f;
+            const float l = warp_sum(w * fabsf(ml.y));
+            const bool far = __any_sync(0xffffffffu, ml.y < 0.f);
+            if (far && !(ml.y < 0.f)) w *= kKvFarDown;
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const float2* o = reinterpret_cast<const float2*>(a.part_o + slot(i) * DP) + lane;
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
                 }
             }
 #pragma unroll
-            for (int v = 0; v < NV; ++v) join_store(a, out_dtype, j.z + row, head_kv, (v * 32 + lane) * 2, acc[v], m, l);
+            for (int v = 0; v < NV; ++v) join_store(a, out_dtype, j.z + row, head_kv, (v * 32 + lane) * 2, acc[v], m, l, far);
         }
         return;
     }
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) red[0][warp] = m;
-        __syncthreads();
+        const bool far = __syncthreads_or(ml[0].y < 0.f || ml[1].y < 0.f || ml[2].y < 0.f);
         m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
         const float ref = m == -INFINITY ? 0.f : m;
         float l = 0.f;
@@ -142,9 +146,9 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
         for (int x = 0; x < 3; ++x) {
             const int i = threadIdx.x + 128 * x;
             if (i >= n) continue;
-            const float w = part_weight(ml[x].x, ref);
-            weight[i] = w;
-            l = fmaf(w, ml[x].y, l);
+            const float w = part_weight(ml[x].x, ref, codes);
+            weight[i] = far && !(ml[x].y < 0.f) ? w * kKvFarDown : w;
+            l = fmaf(w, fabsf(ml[x].y), l);
         }
         l = warp_sum(l);
         if (lane == 0) red[1][warp] = l;
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int ro
                 s.x += sums[x][threadIdx.x].x;
                 s.y += sums[x][threadIdx.x].y;
             }
-            join_store(a, out_dtype, j.z + row, head_kv, threadIdx.x * 2, s, m, l);
+            join_store(a, out_dtype, j.z + row, head_kv, threadIdx.x * 2, s, m, l, far);
         }
         __syncthreads();
     }

@@ -33,7 +33,7 @@
 // warp's tokens of a tile take their weights times b_j / b (b the power of two above the
 // largest of their scales; up to 16, 32 or 64 tokens share one) into the product, and the product is
 // multiplied by b: a block whose scale is far below its neighbours' loses what that
-// ratio takes from the 2^-51.
+// ratio takes from the 2^-51.  Sums of values of any size are finite: see kKvFarPower.
 //
 // Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens, 16 query
 // heads over 8, 545 MB: 95 us, 5.7 TB/s (fp32 queries 96; heads of 64, half the bytes, 74; of
@@ -244,6 +244,7 @@ struct Smem8 {
     float2* stats;    // [4][16]: a warp's reference and sum of its rows
     float2* rows;     // [64]: the rows' reference and sum after the join
     float* row_unit;  // [64]: power of two that a row of queries was scaled down by
+    float* out_unit;  // [4]: what a warp's output is held times (1 or kKvFarDown)
 };
 
 // What a row of queries whose largest magnitude is `big` is multiplied by, and its
@@ -272,6 +273,28 @@ __device__ __forceinline__ float largest4(float4 v) {
     return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 }
 
+// This tile's value scales (exponent `be`) are the warp's first far ones (kv.h): its unit from now on,
+// and what the tile's products and the outputs before it are multiplied by.  How it is
+// reached is chosen by what it costs tiles without such scales (registers): within the edges'
+// branch, as a call where registers spill anyway (8 .. 32 rows of heads of 128 69 us, inlined 70
+// .. 75; fp32 queries 81, inlined 94), inlined up to eight rows (64 sequences 95.6, as a call 96.6).
+template <int RG>
+__device__ __forceinline__ void go_far(uint32_t be, float* unit, float& b, float (&f)[RG][2]) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *unit = kKvFarDown;
+    __syncwarp();
+    b = __uint_as_float(be << 23) * (2.f * kKvFarDown);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+        f[g][0] *= kKvFarDown;
+        f[g][1] *= kKvFarDown;
+    }
+}
+template <int RG>
+__device__ __noinline__ void go_far_call(uint32_t be, float* unit, float& b, float (&f)[RG][2]) {
+    go_far(be, unit, b, f);
+}
+
 // One pair's tiles w.tile .. w.tile + nt - 1 by the four compute warps, WR of them
 // along the rows (8 RG rows each) and 4 / WR along a tile's tokens; the result goes
 // to the output (`whole`) or to slot `part` of the workspace.
@@ -287,6 +310,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
     constexpr int ND = DP / 16;     // 16-column blocks of the output
     constexpr int KS = DP / 16;     // steps along the head dimension of a score
     static_assert(8 * RG * WR <= ROWS, "the row groups lie within a row tile");
+    constexpr bool kCall = ROWS > 8;  // of go_far
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wr = warp % WR, wt = warp / WR;
     const int quad = lane >> 2, qc = lane & 3;
@@ -394,6 +418,8 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
         m[g][0] = m[g][1] = -INFINITY;
         l[g][0] = l[g][1] = 0.f;
     }
+    if (lane == 0) sm.out_unit[warp] = 1.f;  // (this warp's alone)
+    __syncwarp();
     const bool active = row0 < w.t.rows;  // a warp whose rows are all padding only keeps the barriers
     int tok0 = (w.t.lo / TILE + w.tile) * TILE + wt * TOK;  // the warp's first token
     // This lane's ldmatrix row in a key and a value tile: 16 tokens of two 16-byte chunks.
@@ -511,15 +537,16 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                         }
                 }
         }
-        // a power of two above the warp's largest value scale, and the scales over it
+        // 2^(be - 126), a power of two above the warp's largest value scale, and the scales over it
         float b = 0.f;
 #pragma unroll
         for (int t = 0; t < MT; ++t) b = fmaxf(b, vb[t]);
         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
-        const uint32_t be = min(__float_as_uint(b) >> 23, 252u);
-        b = __uint_as_float((be + 1u) << 23);
+        const uint32_t be = min(max(__float_as_uint(b) >> 23, 1u), 254u);
+        const float over = __uint_as_float((255u - be) << 23) * 0.25f;  // (subnormal for scales from 2^126 on)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) vb[t] *= __uint_as_float((253u - be) << 23);
+        for (int t = 0; t < MT; ++t) vb[t] *= over;
+        b = __uint_as_float(be << 23) * (2.f * sm.out_unit[warp]);
         float f[RG][2];
         uint32_t pb[MT][RG][PP][2];  // P^T in fp16 parts, as the B operand
 #pragma unroll
@@ -561,7 +588,14 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
         }
         if (ok) ok = tile_wait(&sm.v_full[vring.slot], vring.parity);
         uint8_t* vtile = sm.v + vring.slot * P::kSlotBytes;
-        if (edge) {
+        const bool far = be > 126u + kKvFarPower, rare = edge || far;
+        if (kCall ? rare : __builtin_expect(rare, 0)) {
+            if (far && sm.out_unit[warp] == 1.f) {
+                if constexpr (kCall)
+                    go_far_call(be, sm.out_unit + warp, b, f);
+                else
+                    go_far(be, sm.out_unit + warp, b, f);
+            }
             // What no row sees counts as zero whatever the cache holds: its codes are
             // cleared in the tile.  A NaN that some rows see must not reach the others
             // as 0 * NaN: it is cleared too once each row that sees it has added it.
@@ -662,7 +696,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
     }
 
     // ---- end of the pair's part in this CTA: the warps that share rows agree on
-    // their reference and sum, and scale to it
+    // their reference, sum and unit, and scale to it
 #pragma unroll
     for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -672,6 +706,8 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
             if (quad == 0) sm.stats[warp * 16 + g * 8 + qc * 2 + x] = make_float2(m[g][x], l[g][x]);
         }
     compute_sync();
+    const float unit = fminf(fminf(sm.out_unit[0], sm.out_unit[1]), fminf(sm.out_unit[2], sm.out_unit[3]));
+    const float to_unit = unit < sm.out_unit[warp] ? kKvFarDown : 1.f;
 #pragma unroll
     for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -687,7 +723,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                 L = fmaf(st.y, exp2_approx(st.x - ref), L);
             }
             if (wt == 0 && quad == 0) sm.rows[row0 + rr] = make_float2(M, L);
-            const float k = exp2_approx(m[g][x] - ref);
+            const float k = exp2_approx(m[g][x] - ref) * to_unit;
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
                 o[n][g][x] *= k;
@@ -730,7 +766,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                     const int flat = w.t.first_row + rr, tok = a.by_group(flat);
                     const int64_t token = w.first + tok;
                     const int head = w.h * a.group + flat - tok * a.group;
-                    const float inv = ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);  // NaN stays NaN
+                    const float inv = (ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y)) / unit;  // NaN stays NaN
                     const int64_t off = token * a.out_stride + static_cast<int64_t>(head) * dim + d;
                     sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
                     if (d < dim) {
@@ -747,7 +783,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
                 } else {
                     const int64_t at = static_cast<int64_t>(part) * ROWS + rr;
                     *reinterpret_cast<float4*>(a.part_o + at * P::kPad + d) = sum;
-                    if (d == 0) a.part_ml[at] = ml;
+                    if (d == 0) a.part_ml[at] = make_float2(ml.x, unit < 1.f ? -ml.y : ml.y);
                 }
             }
         }
@@ -765,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t k_full[KSLOTS], k_empty[KSLOTS], v_full[VSLOTS], v_empty[VSLOTS];
     __shared__ float2 stats[kComputeWarps * 16], rows[64];
-    __shared__ float row_unit[64], scales[KSLOTS * 32];
+    __shared__ float row_unit[64], scales[KSLOTS * 32], out_unit[kComputeWarps];
     uint8_t* q_smem = base + P::kSlots * P::kSlotBytes;
     const Smem8 sm = {base,   base + KSLOTS * P::kSlotBytes,
                       scales, q_smem,
@@ -773,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, Plan8<DP, ROWS, QF32>::kCtasPerSm)
                       k_full, k_empty,
                       v_full, v_empty,
                       stats,  rows,
-                      row_unit};
+                      row_unit, out_unit};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
