@@ -524,10 +524,11 @@ mnb_status kv_attention_workspace_size(int64_t q_heads, int64_t kv_heads, int64_
  * the row's largest, smaller ones err by 2^-50 of it, and where up to 64
  * neighbouring tokens' value scales differ, the smaller ones' probabilities have
  * these limits raised by the ratio to the largest (whether the row sees its token
- * or not).  Values of any size give finite sums; a value past fp32's largest
- * number counts as it is, up to the rounding of out.  A NaN code that a row sees gives
- * NaN.  Scales of blocks without a visible token are not read; the others are
- * finite and not negative (a scale that is not spoils the rows that see its block).
+ * or not).  Keys of any size give the scores that fp32 holds, values of any size
+ * finite sums; a value past fp32's largest number counts as it is, up to the
+ * rounding of out.  A NaN code that a row sees gives NaN.  Scales of blocks
+ * without a visible token are not read; the others are finite and not negative
+ * (a scale that is not spoils the rows that see its block).
  * Made for a few new tokens per sequence (decoding, drafts): one pass over the
  * cache serves 64 rows, so that a prompt is right but re-reads it.  workspace
  * 256-byte aligned. */

@@ -123,6 +123,7 @@ struct KvAttnArgs {
     int group;   // query heads per key-value head
     FastDiv by_group, by_page;  // division by group, by the page size
     float scale;
+    float scale_unit, scale_rest;  // over 8-bit codes: a power of two, and scale * log2(e) over it (1.4 .. 2.9)
     int q_dtype;
     int window;  // 0: every earlier token
     int box_rows;

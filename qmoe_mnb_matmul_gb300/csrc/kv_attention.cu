@@ -1,6 +1,7 @@
 // kv_attention.cu -- host side of the paged attention (see
 // kv_attention_impl.cuh) and the kernel that joins the parts of split pairs.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "common.cuh"
@@ -262,6 +263,9 @@ cudaError_t launch_kv_attention(const KvAttnArgs& in, int q_dtype, int64_t max_n
     a.by_group.set(static_cast<uint32_t>(a.group));
     a.by_page.set(static_cast<uint32_t>(a.cache.page_size));
     a.q_dtype = q_dtype;
+    int power;
+    a.scale_rest = std::frexp(a.scale, &power) * 2.f * 1.4426950408889634f;
+    a.scale_unit = std::ldexp(1.f, power - 1);
     const bool codes = a.cache.dtype == MNB_E4M3;
     // a TMA box holds as many rows as divide a page (at least 8, at most a tile)
     a.box_rows = codes ? kv_tile8(rows, pad) : kKvTile;

@@ -316,18 +316,17 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
     const int quad = lane >> 2, qc = lane & 3;
     const int dim = a.cache.dim;
     const int row0 = wr * 8 * RG;  // the warp's first row of the row tile
-    const float scale2 = a.scale * 1.4426950408889634f;  // scores to log2 units
     constexpr int kShift = kv_weight_shift(MNB_E4M3);
 
     // ---- queries: lane holds elements 4 qc .. 4 qc + 3 of each sixteen of row quad of each eight
     uint32_t qf[P::kQSmem ? 1 : KS][PQ][2];
-    float c[RG][2];  // scores to log2 units, rows 2 qc and 2 qc + 1 of each eight
+    float c[RG][2];  // powers of two of the queries and the scale, rows 2 qc and 2 qc + 1 of each eight
     auto q_at = [&](int rr) {  // element offset of row rr's query
         const int flat = w.t.first_row + rr, tok = a.by_group(flat);
         return (w.first + tok) * a.q_stride + static_cast<int64_t>(w.h * a.group + flat - tok * a.group) * dim;
     };
-    // never 0 or infinite: a score of -inf (unseen) or 0 times it stays what it is
-    auto factor = [&](float up) { return fminf(fmaxf(scale2 * up, __uint_as_float(1u)), 3.402823466e38f); };
+    // (rounded towards zero: never infinite, so that a score of 0 times it stays 0)
+    auto factor = [&](float up) { return __fmul_rz(a.scale_unit, up); };
     if constexpr (!P::kQSmem) {
         static_assert(P::kQSmem || (RG == 1 && WR == 1), "eight rows");
         const bool in = quad < w.t.rows;
@@ -509,7 +508,8 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         if constexpr (QF32 || kTwo) s[t][g][x] += s2[t][g][x];
-                        s[t][g][x] *= ka[t];
+                        // (the two powers first: a key's may pass 2^96, where the row's brings the score back)
+                        s[t][g][x] *= __fmul_rz(ka[t], c[g][x & 1]);
                     }
         }
         tile_free(&sm.k_empty[kring.slot], lane);
@@ -560,7 +560,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
                 // rounded up, so that no weight passes 2^shift
-                big = fmaxf(m[g][x], __fmaf_ru(big, c[g][x], -kShift));
+                big = fmaxf(m[g][x], __fmaf_ru(big, a.scale_rest, -kShift));
                 // a row that has seen nothing yet keeps a zero reference, so that its exponentials are 2^-inf = 0
                 ref[x] = big == -INFINITY ? 0.f : big;
                 f[g][x] = exp2_approx(m[g][x] - ref[x]);
@@ -574,7 +574,7 @@ __device__ __forceinline__ void run_part8(const KvAttnArgs& a, const Smem8& sm, 
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         float& e = s[t][g][2 * y + x];
-                        e = exp2_approx(fmaf(e, c[g][x], -ref[x]));
+                        e = exp2_approx(fmaf(e, a.scale_rest, -ref[x]));
                         sum[x] += e;
                         e *= vb[t];
                     }

@@ -69,3 +69,51 @@ def test_ordinary_values_beside_huge_ones_of_no_weight(group, new, length, first
     out, lse = run(bt, q)
     ref, rlse, (A, V) = reference(bt, q, group, 64 ** -0.5, 0)
     check(bt, q, out, lse, group, 64 ** -0.5, 0, "f32")
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("length", [60, 2048, 40001])
+@pytest.mark.parametrize("power,spread", [(100, 2.0 ** -107), (119, 2.0 ** -126), (60, 2.0 ** -67), (-60, 2.0 ** 53),
+                                          (-126, 2.0 ** 119), (-100, 2.0 ** 93)])
+def test_keys_of_any_magnitude_with_queries_that_bring_the_scores_back(group, new, length, power, spread):
+    g = rng("keys", group, new, length, power)
+    bt = Codes(g, [length], [new], 1, 128, 16, 16)
+    bt.fill(g)
+    bt.k.copy_(codes(g, bt.k, 400))
+    bt.ks.fill_(2.0 ** power)
+    q = torch.randn((new, group, 128), generator=g, device="cuda") * spread
+    out, lse = run(bt, q)
+    check(bt, q, out, lse, group, 128 ** -0.5, 0, "f32")
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("power", [97, 110, 117])
+def test_keys_that_leave_one_token(group, new, power):
+    """Scores of up to 2^126: the largest takes all."""
+    g = rng("one token", group, new, power)
+    bt = Codes(g, [200], [new], 1, 64, 16, 16)
+    bt.fill(g)
+    bt.k.fill_(0x38)                                        # 1
+    bt.ks.fill_(2.0 ** power)
+    page, row = bt.place(0, 77)
+    bt.k[page, :, row] = 0x40                               # 2
+    q = torch.ones((new, group, 64), device="cuda")
+    out, lse = run(bt, q)
+    _, v = bt.rows_of(0, 0)
+    assert bool(((out.double() - v[77]).abs() <= 2.0 ** -20 * v[77].abs()).all())
+    assert bool((lse == 2.0 ** (power + 4)).all())          # 64^-0.5 * 64 * 2 * 2^power
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("scale,spread", [(1e-30, 1e-16), (1e-38, 1e-30), (2.0 ** -149, 1.0), (1e-31, 1e31), (1e-37, 1e37),
+                                          (1e31, 1e-31), (1e36, 1e-37)])
+def test_queries_and_scales_of_any_magnitude(dtype, group, new, scale, spread):
+    """Queries far from 1 with a scale that brings the scores back, or that leaves nothing of them."""
+    g = rng("magnitude", dtype, group, new, scale)
+    bt = Codes(g, [300, 65, 1], [new, new, 1], 2, 128, 16, 16)
+    bt.fill(g)
+    q = (torch.randn((bt.tokens, 2 * group, 128), generator=g, device="cuda") * spread).to(DT[dtype])
+    q[0, 0] = 0.0
+    out, lse = run(bt, q, scale=scale)
+    check(bt, q, out, lse, group, float(torch.tensor(scale)), 0, dtype)
