@@ -105,9 +105,11 @@ __device__ __forceinline__ float2 power2(float2 x, float2 minus_ref, float2 scal
     x = ffma2(x, scale, make_float2(-0.f, -0.f));
     return make_float2(exp2_fast(x.x), exp2_fast(x.y));
 }
+// (Two products and a sum, not one fused: the same bits with a and b exchanged, so that after an
+// exchange in pairs every lane and CTA of a row holds the same sum.)
 __device__ __forceinline__ Soft join(const Soft& a, const Soft& b, float scale) {
     const float top = fmaxf(a.top, b.top), ref = reference(top);
-    return {top, fmaf(a.sum, power(a.top, ref, scale), b.sum * power(b.top, ref, scale))};
+    return {top, __fadd_rn(__fmul_rn(a.sum, power(a.top, ref, scale)), __fmul_rn(b.sum, power(b.top, ref, scale)))};
 }
 // A running argmax: the largest value and its first place; a NaN anywhere shows as place -1.
 struct First {

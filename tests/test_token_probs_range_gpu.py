@@ -25,3 +25,25 @@ def test_row_starts_at_the_end_of_32_bits(V):
     check(out, r, rows=[4, 0, 0])
     assert bool((out[1:] == 7.0).all())
     assert mnb.mnb_get_last_device_error() == 0
+
+
+@pytest.mark.parametrize("B,V", [(1, 151936), (3, 50257), (8, 32000), (64, 30001)])
+@pytest.mark.parametrize("seed", range(4))
+def test_equal_logits_get_equal_probabilities(B, V, seed):
+    """Tokens of one logit in every lane, warp and CTA, whose own sums and largest values differ; some come to that
+    logit by a bias (both numbers and their sum are whole), so that they are joined apart."""
+    r = inputs(seed, B, 2, V, "f32", penalties=False)
+    r["logits"][..., 5::37] = 3.0
+    listed = torch.arange(17, V, 331, dtype=torch.int32, device="cuda")[:90]
+    r["logits"][..., listed.long()] = -2.0
+    r["bias_tokens"] = listed.expand(B, -1).contiguous()
+    r["bias_values"] = torch.full((B, len(listed)), 5.0, device="cuda")
+    out = torch.empty((B, 2, V), device="cuda")
+    mnb.token_probs(r["logits"], rules(r, B), out)
+    equal = torch.zeros(V, dtype=torch.bool, device="cuda")
+    equal[5::37] = True
+    equal[listed.long()] = True
+    p = out[..., equal]
+    assert bool((p > 0).all()) and bool((p == p[..., :1]).all())
+    for b in range(0, B, 16):
+        check(out[b:b + 1], {k: v[b:b + 1] for k, v in r.items() if v is not None})
