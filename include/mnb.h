@@ -578,7 +578,8 @@ typedef struct {
  *            between sequences and rows, or with row_start [batch + 1] a ragged
  *            step's [tokens, vocab] rows: row i of sequence b is row row_start[b] + i,
  *            those with row_start[b] + i < row_start[b + 1] exist, and the others
- *            of out are left alone.
+ *            of out are left alone.  So are rows that would exist outside [0, tokens)
+ *            or of a row_start[b] below 0, which record MNB_ERR_CONTENT.
  *   draft_tokens [batch, rows - 1] or NULL.
  *   mask     or NULL: bit v % 32 of word v / 32 of a row's ceil(vocab / 32) words
  *            is 1 where v is allowed; strides in words (0 shares a row).

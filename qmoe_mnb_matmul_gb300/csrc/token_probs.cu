@@ -173,7 +173,11 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
     const T* logits = static_cast<const T*>(a.logits);
     if (a.row_start) {
         const int64_t r0 = __ldg(a.row_start + b), r1 = __ldg(a.row_start + b + 1), r = r0 + i;  // (r passes 32 bits where r0 ends there)
-        if (r0 < 0 || r >= r1 || r >= a.tokens) return;  // (the whole cluster)
+        if (r >= r1) return;  // (the whole cluster, here and below)
+        if (r0 < 0 || r >= a.tokens) {
+            if (rank == 0 && tid == 0) record_error(MNB_ERR_CONTENT);
+            return;
+        }
         logits += r * a.logits_row;
     } else {
         logits += b * a.logits_seq + i * a.logits_row;

@@ -11,6 +11,8 @@ if not torch.cuda.is_available():
 import qmoe_mnb_matmul_gb300 as mnb  # noqa: E402
 from tests.test_token_probs_gpu import check, inputs, rules  # noqa: E402
 
+CONTENT = 7
+
 
 @pytest.mark.parametrize("V", [1000, 2001])
 def test_row_starts_at_the_end_of_32_bits(V):
@@ -47,3 +49,33 @@ def test_equal_logits_get_equal_probabilities(B, V, seed):
     assert bool((p > 0).all()) and bool((p == p[..., :1]).all())
     for b in range(0, B, 16):
         check(out[b:b + 1], {k: v[b:b + 1] for k, v in r.items() if v is not None})
+
+
+def test_rows_that_the_logits_do_not_have_are_reported():
+    """A sequence's rows that lie outside the step's logits: their probabilities are left alone, and the error word says
+    so.  Rows that a sequence does not ask for are no error."""
+    V, B, R = 1500, 3, 3
+    r = inputs(9, B, R, V, "bf16")
+    r["logits"] = r["logits"].flatten(0, 1)[:5].contiguous()
+    d = rules(r, B)
+
+    def run(*start):
+        out = torch.full((B, R, V), 7.0, device="cuda")
+        mnb.token_probs(r["logits"], d, out, row_start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+        return out, mnb.mnb_get_last_device_error()
+
+    whole, error = run(0, 2, 2, 5)
+    assert error == 0
+    check(whole, r, rows=[2, 0, 3])
+    out, error = run(0, 2, 2, 6)             # sequence 2 has four rows, three places in out: no row past the logits
+    assert error == 0 and torch.equal(out, whole)
+    out, error = run(0, 2, 3, 6)             # the last row of sequence 2 is row 5 of 5
+    assert error == CONTENT
+    assert bool((out[2, 2] == 7.0).all()) and bool((out[1, 1:] == 7.0).all()) and torch.equal(out[0], whole[0])
+    out, error = run(-2, 2, 2, 5)            # sequence 0 begins before the logits
+    assert error == CONTENT
+    assert bool((out[0] == 7.0).all()) and torch.equal(out[1:], whole[1:])
+    out, error = run(7, 7, 7, 7)             # no rows at all
+    assert error == 0 and bool((out == 7.0).all())
+    out, error = run(0, 2, 2, 5)
+    assert error == 0 and torch.equal(out, whole)
