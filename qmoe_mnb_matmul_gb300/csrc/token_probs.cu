@@ -413,8 +413,9 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
         return;
     }
     if (!greedy) {
-        // values to log2 units; finite and not zero, so that neither 0 times it nor -inf times it is NaN
-        const float scale = fminf(fmaxf(1.4426950408889634f / temperature, 1.17549435e-38f), 3.402823466e38f);
+        // values to log2 units; finite and not zero, so that neither 0 times it nor -inf times it is
+        // NaN (subnormal for temperatures from 1.3e38 on, 2^-149 for an infinite one)
+        const float scale = fminf(fmaxf(1.4426950408889634f / temperature, __uint_as_float(1u)), 3.402823466e38f);
         Soft mine = {-INFINITY, 0.f};
         pass(Count<4>{}, false, [&](int, auto& x) {
             float top = mine.top;

@@ -9,7 +9,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import qmoe_mnb_matmul_gb300 as mnb  # noqa: E402
-from tests.test_token_probs_gpu import check, inputs, rules  # noqa: E402
+from tests.test_token_probs_gpu import DT, check, inputs, rules  # noqa: E402
 
 CONTENT = 7
 
@@ -79,3 +79,25 @@ def test_rows_that_the_logits_do_not_have_are_reported():
     assert error == 0 and bool((out == 7.0).all())
     out, error = run(0, 2, 2, 5)
     assert error == 0 and torch.equal(out, whole)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("temperature", [1e30, 1e37, 1.2e38, 2e38, 3.4e38])
+def test_temperatures_as_large_as_the_logits(dtype, temperature):
+    """(x - m) / T is of the order of one: its two roundings are 2^-24 of at most 4 each and the logarithm's base a
+    third, the exponential and the sum err by a few 2^-22."""
+    r = inputs(11, 2, 2, 3001, "f32", penalties=False)
+    r["logits"] = (r["logits"].clamp(-7, 7) / 7 * min(1.6e38, 2 * temperature)).to(DT[dtype])
+    r["temperature"] = torch.tensor([temperature, 1.0], device="cuda")
+    out = torch.empty((2, 2, 3001), device="cuda")
+    mnb.token_probs(r["logits"], rules(r, 2), out)
+    check(out, r, rel=2.0 ** -18)
+
+
+def test_an_infinite_temperature_leaves_the_row_even():
+    x = torch.tensor([[[1.0, -3e38, 2e37, 0.0]]], device="cuda")
+    out = torch.empty_like(x)
+    mnb.token_probs(x, mnb.token_rules(temperature=torch.full((1,), float("inf"), device="cuda")), out)
+    # 1 / T is held as fp32's smallest number, 2^-149, so that -infinity times it stays that: differences of less than
+    # 2^129 come out as exponents below 2^-20
+    assert bool(((out - 0.25).abs() <= 0.25 * 2.0 ** -19).all())
