@@ -23,11 +23,14 @@
 // warps on an SM, made prompts of 16920 tokens 92 us instead of 83).  The rows' angles are
 // neighbours in the table: one bulk copy per block brings them to shared memory.
 //
-// Bound: instruction issue (57 %, 24 instructions an element over all) and load latency for
+// Bound: instruction issue (63 % of active cycles, 25 instructions an element over all) and load latency for
 // prompts, three dependent loads for one token.
 //
-// Measured: one token of 16 + 8 + 8 heads of 128 in fp32 4.9 us, 190 drafts of 64 sequences 7.5
-// us; prompts of 16920 tokens in bf16 74 us, 3.4 TB/s (251 MB).  Sixteen tokens a warp at
+// Measured: one token of 16 + 8 + 8 heads of 128 in fp32 5.0 us, 190 drafts of 64 sequences 7.5
+// us where their blocks' scales stand, 6.5 and 10.4 where every block's scale grows (its older codes
+// are read once the largest value is known); prompts of 16920 tokens in bf16 74 us, 3.4 TB/s (251 MB).
+// The append to a 16-bit cache is faster in each (2.5, 3.6 and 56 us): it does a token's work where this one
+// does a block's, and packed arithmetic.  Sixteen tokens a warp at
 // 128 registers took 110 us, angles from global memory 3 us more of a short call.
 #include <algorithm>
 

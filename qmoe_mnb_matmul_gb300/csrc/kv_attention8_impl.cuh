@@ -36,13 +36,19 @@
 // ratio takes from the 2^-51.  Sums of values of any size are finite: see kKvFarPower.
 //
 // Measured (GB300, heads of 128, join included): 64 sequences of 1 .. 8192 tokens, 16 query
-// heads over 8, 545 MB: 95 us, 5.7 TB/s (fp32 queries 96; heads of 64, half the bytes, 74; of
-// 256, 4 over 16, 54); one sequence of 131072 tokens, 32 over 4, 134 MB: 33.5 us; 777 tokens: 7.9 us, all
+// heads over 8, 545 MB: 95 us, 5.7 TB/s (fp32 queries 96; heads of 64, half the bytes, 73.5); 32 such
+// sequences, 16 heads of 256 over 4, 274 MB: 54.6 us, 5.0 TB/s (fp32 59); one sequence of 131072
+// tokens, 32 over 4, 134 MB: 33.9 us; 777 tokens: 8.0 us, all
 // latency.  A tile takes 1.3 us and 0.2 us more per 4 KB of it: bound by the chain of a
-// tile's steps in two compute warps per scheduler (issue slots 48 % busy), not by the
-// tensor pipe (22 %) or HBM.  16 sequences with 1 .. 5 drafts, 8 .. 40 rows, 147 MB: 88 us (spills
-// of 88 .. 384 bytes at 168 registers; 692 with fp32 queries), with 4 .. 20 rows of heads of 80
-// and a window, 57 MB: 39 us.  What was slower: one producer warp for keys, values and scales (153 us for the
+// tile's steps in two compute warps per scheduler (issue slots 46 % of active cycles busy), not by the
+// tensor pipe (25 %) or HBM (72 %).
+// Several rows, 32 query heads over 4, 147 MB: 16 sequences of 8 .. 16 rows 50.4 us, of 8 .. 32
+// rows 69 (fp32 queries 83), of 8 .. 40 rows 95 (fp32 132; over a 16-bit cache, with twice the bytes, 82:
+// warps that split along the rows each convert the whole tile); of 4 .. 20 rows of heads of 80
+// with a window, 57 MB: 41.4 us (fp32 46).  A prompt of 2048 tokens, 16 over 8: 266 us.  Spills, of 16-bit
+// (fp32) queries at 168 registers: tiles of 32 rows 60 .. 96 (64 .. 324) bytes, of 64 rows 112 .. 436
+// (256 .. 728), of eight rows none (up to 72).
+// What was slower: one producer warp for keys, values and scales (153 us for the
 // batch), three CTAs per SM with it (122) or with spills at 96 registers, the scores
 // of the next tile among this one's products (105).
 #pragma once
@@ -84,6 +90,7 @@ struct Plan8 {
 // and three, 15.5 with four; 200 of 10 .. 300 48.8, 47.6, 48.5 with two, three, four.
 // With more rows a tile's cost grows with them (of 64 tokens: 4 units up to 8 rows, 12 for 33 and
 // more): 16 sequences of 4 .. 20 rows, heads of 80, 50 us with one unit for all, 42 with these.
+// (All of it over 16-bit queries of heads of 80 and 128; fp32 queries and other widths go by the same.)
 template <int ROWS>
 struct Costs8 {
     static constexpr int kMost = ROWS == 8 ? 1 : ROWS == 32 ? 7 : 12, kPair = ROWS == 8 ? 4 : 16;

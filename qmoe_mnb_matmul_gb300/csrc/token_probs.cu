@@ -29,7 +29,8 @@
 //
 // Measured (151936 entries): one sequence of 5 fp32 rows with 2000 tokens of history 9.8 us (one
 // row without lists 6.1), 64 sequences of up to 6 bf16 rows with 3000 tokens, biases and
-// masks, 208 MB: 73 us, 2.8 TB/s; 64 fp32 rows without lists, 78 MB: 23 us.  A row has three phases with
+// masks, 208 MB: 73 us, 2.8 TB/s (all greedy 92, changed logits alone 102); 64 fp32 rows without lists, 78 MB:
+// 23 us (greedy 28.5, logits 18).  A row has three phases with
 // a barrier of its cluster between them, and two CTAs of 512 threads per SM do not
 // cover each other's (issue 46 %, DRAM 32 %, 89 MB read for 67).  256 threads, 1024, and three or four
 // CTAs per SM with fewer registers were slower, one kernel that keeps the row in registers too (245 us).
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const Prob
     const int groups = cdiv(vocab, static_cast<int>(ctas) * kProbWarps * 128);
     auto chunk = [&](int k) { return (k * kProbWarps + warp) << ctas_log | static_cast<int>(rank); };
     auto place = [&](int k, int j) { return chunk(k) * 128 + (VEC ? lane * 4 + j : j * 32 + lane); };
-    // (the first group's logits on their way to L2 while the lists are read)
+    // (the row's logits on their way to L2 while the lists are read)
     for (int k = 0; k < groups; ++k) {
         const int at = chunk(k) * 128 + lane * static_cast<int>(128 / sizeof(T));
         if (lane < static_cast<int>(sizeof(T)) && at < vocab)
@@ -514,7 +515,7 @@ cudaError_t launch_token_probs(const ProbArgs& a, int dtype, int sm_count, bool 
                      a.out_seq % 4 == 0 && a.out_row % 4 == 0;
     const int64_t listed = (a.history ? a.history_columns : 0) + (a.draft_tokens ? a.rows - 1 : 0) + a.biases;
     // CTAs per row: up to about three per SM in all, so that one's loads cover another's exchange (222
-    // rows of 151936 entries with lists: 70 us in twos, 86 in fours, 113 in eights; 5 rows
+    // rows of 151936 entries with lists, measured side by side: 70 us in twos, 86 in fours, 113 in eights; 5 rows
     // 9.6 in sixteens, 11.3 in eights); no more than there are tokens for, and
     // more where the lists would not leave room for two on an SM
     const int64_t rows = a.row_start ? std::min(a.batch * a.rows, a.tokens) : a.batch * a.rows;
