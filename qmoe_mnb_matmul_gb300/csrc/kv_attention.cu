@@ -45,7 +45,8 @@ namespace {
 // The parts come from L2 (2.5 MB in all with
 // 8-row tiles); what it costs is the launch and two dependent loads (the record,
 // then the first parts together with the statistics), so it is kept small: eight
-// rows at a time in 256 threads took 2.4 us longer.
+// rows at a time in 256 threads took 2.4 us longer, 72 registers instead of 56 (seven CTAs per
+// SM instead of nine) 3 us of 95 for drafts of 24 .. 40 rows.
 constexpr int kFewParts = 16;
 constexpr int kJoinGridY = 16;  // CTAs of a pair
 
@@ -74,7 +75,7 @@ __device__ __forceinline__ float part_weight(float reference, float largest, boo
 }
 
 template <int DP>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int rows_per_tile, int out_dtype) {
+__global__ void __launch_bounds__(128, DP == 128 ? 9 : 7) kv_join_kernel(const KvAttnArgs a, int rows_per_tile, int out_dtype) {
     constexpr int NV = DP / 64;    // float2 per lane
     constexpr int AHEAD = 8 / NV;  // parts of a warp asked for before their weights are known
     __shared__ float weight[kKvMaxCtas];

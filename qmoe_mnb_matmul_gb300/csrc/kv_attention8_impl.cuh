@@ -43,9 +43,9 @@
 // tile's steps in two compute warps per scheduler (issue slots 46 % of active cycles busy), not by the
 // tensor pipe (25 %) or HBM (72 %).
 // Several rows, 32 query heads over 4, 147 MB: 16 sequences of 8 .. 16 rows 50.4 us, of 8 .. 32
-// rows 69 (fp32 queries 83), of 8 .. 40 rows 95 (fp32 132; over a 16-bit cache, with twice the bytes, 82:
+// rows 69 (fp32 queries 82), of 8 .. 40 rows 92 (fp32 132; over a 16-bit cache, with twice the bytes, 82:
 // warps that split along the rows each convert the whole tile); of 4 .. 20 rows of heads of 80
-// with a window, 57 MB: 41.4 us (fp32 46).  A prompt of 2048 tokens, 16 over 8: 266 us.  Spills, of 16-bit
+// with a window, 57 MB: 40.3 us (fp32 44).  A prompt of 2048 tokens, 16 over 8: 265 us.  Spills, of 16-bit
 // (fp32) queries at 168 registers: tiles of 32 rows 60 .. 96 (64 .. 324) bytes, of 64 rows 112 .. 436
 // (256 .. 728), of eight rows none (up to 72).
 // What was slower: one producer warp for keys, values and scales (153 us for the
